@@ -1,4 +1,5 @@
-"""Python binding of libimgstencil: direct 2D convolution with small filters on gfx950.
+"""Python binding of libimgstencil: direct 2D convolution with small filters on gfx950,
+and the attention operators of networks that attend between their convolution layers.
 
 The functions with the C names (conv2d_create, conv2d_forward, conv2d_destroy,
 conv2d_get_plan_info, conv2d_list_variants, conv2d_create_variant,
@@ -7,20 +8,30 @@ conv_chain_kernel_name, conv_chain_groups, is_lds_tile_bytes, is_swizzle_col,
 is_persistent_grid) marshal arguments to
 the C ABI of include/imgstencil.h and nothing else. conv2d() and conv_chain()
 are conveniences on torch tensors: torch only allocates device memory and
-supplies the current HIP stream.
+supplies the current HIP stream. The attention operators (Rotary,
+CrossAttention, rotary(), qk_norm_rotary(), cross_attention() and their C names)
+are in attention.py.
 """
 import ctypes
 
 from . import _abi
 from ._abi import (IS_F16, IS_F32, IS_NCHW, IS_NHWC, IS_CHAIN_AUTO, IS_CHAIN_FUSED, IS_CHAIN_UNFUSED,
                    ImgStencilError, conv2d_desc, conv_chain_desc, conv2d_plan_info, conv2d_variant)
+from .attention import (CrossAttention, Rotary, cross_attention, cross_attention_create, cross_attention_destroy,
+                        cross_attention_forward, cross_attention_get_plan_info, cross_attention_workspace_size,
+                        qk_norm_rotary, qk_norm_rotary_forward, rotary, rotary_create, rotary_destroy,
+                        rotary_forward, rotary_get_frequencies)
 
 __all__ = ["conv2d_create", "conv2d_forward", "conv2d_destroy", "conv2d_get_plan_info",
            "conv2d_list_variants", "conv2d_create_variant", "conv2d_autotune",
            "conv_chain_workspace_size", "conv_chain_forward", "conv_chain_forward_noalloc",
            "conv_chain_kernel_name", "conv_chain_groups",
            "is_lds_tile_bytes", "is_swizzle_col", "is_persistent_grid", "is_version", "make_desc", "make_chain_desc",
-           "conv2d", "conv2d_separable", "conv_chain", "Plan", "ImgStencilError"]
+           "conv2d", "conv2d_separable", "conv_chain", "Plan", "ImgStencilError",
+           "rotary_create", "rotary_destroy", "rotary_get_frequencies", "rotary_forward", "qk_norm_rotary_forward",
+           "cross_attention_create", "cross_attention_destroy", "cross_attention_workspace_size",
+           "cross_attention_get_plan_info", "cross_attention_forward",
+           "Rotary", "CrossAttention", "rotary", "qk_norm_rotary", "cross_attention"]
 
 
 def load():

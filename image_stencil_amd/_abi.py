@@ -11,9 +11,13 @@ LIB_PATH = os.path.join(HERE, "libimgstencil.so")
 
 IS_OK, IS_ERR_INVALID_ARG, IS_ERR_UNSUPPORTED, IS_ERR_MISALIGNED, IS_ERR_HIP, IS_ERR_NO_MEMORY, \
     IS_ERR_WORKSPACE = range(7)
-IS_F32, IS_F16 = 0, 1
+IS_F32, IS_F16, IS_BF16 = 0, 1, 2
 IS_NCHW, IS_NHWC = 0, 1
 IS_CHAIN_AUTO, IS_CHAIN_FUSED, IS_CHAIN_UNFUSED = 0, 1, 2
+IS_ROTARY_HALF, IS_ROTARY_INTERLEAVED = 0, 1
+IS_ROTARY_UNSCALED, IS_ROTARY_LINEAR, IS_ROTARY_NTK, IS_ROTARY_RAMP = 0, 1, 2, 3
+IS_NORM_RMS, IS_NORM_LAYER = 1, 2
+IS_MAX_HEAD_DIM = 256
 IS_MAX_CHAIN = 8
 IS_NOALLOC_MAX_WORKSPACE = 256 << 20
 
@@ -49,6 +53,29 @@ class conv_chain_desc(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("mode", ctypes.c_int)]
 
 
+class is_tokens(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("len", ctypes.c_int), ("heads", ctypes.c_int),
+                ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class rotary_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("d", "rot", "axes", "layout", "scaling", "original_len")] + \
+               [(f, ctypes.c_double) for f in ("base", "factor", "ramp_low", "ramp_high", "magnitude")]
+
+
+class qk_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("q", is_tokens),
+                ("k", is_tokens), ("q_out", is_tokens), ("k_out", is_tokens),
+                ("q_pos_batch_stride", ctypes.c_int64), ("k_pos_batch_stride", ctypes.c_int64)]
+
+
+class cross_attention_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("n", "lq", "lk", "hq", "hkv", "d", "dtype")] + \
+               [("scale", ctypes.c_float)] + \
+               [(f, ctypes.c_int64 * 3) for f in ("q_stride", "k_stride", "v_stride", "out_stride")] + \
+               [("mask_batch_stride", ctypes.c_int64)]
+
+
 # (name, restype, argtypes) of every function the header declares.
 _vp = ctypes.c_void_p
 SIGNATURES = [
@@ -70,6 +97,18 @@ SIGNATURES = [
     ("conv_chain_kernel_name", ctypes.c_int, [ctypes.POINTER(conv_chain_desc), ctypes.c_char_p, ctypes.c_size_t]),
     ("conv_chain_groups", ctypes.c_int, [ctypes.POINTER(conv_chain_desc), ctypes.POINTER(ctypes.c_int), ctypes.c_int,
                                          ctypes.POINTER(ctypes.c_int)]),
+    ("rotary_create", ctypes.c_int, [ctypes.POINTER(rotary_desc), ctypes.POINTER(_vp)]),
+    ("rotary_destroy", None, [_vp]),
+    ("rotary_get_frequencies", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_double), ctypes.c_int,
+                                              ctypes.POINTER(ctypes.c_int)]),
+    ("rotary_forward", ctypes.c_int, [_vp, ctypes.c_int, ctypes.POINTER(is_tokens), _vp, _vp, ctypes.c_int64,
+                                      ctypes.POINTER(is_tokens), _vp, _vp]),
+    ("qk_norm_rotary_forward", ctypes.c_int, [_vp, ctypes.POINTER(qk_norm_desc)] + [_vp] * 9),
+    ("cross_attention_create", ctypes.c_int, [ctypes.POINTER(cross_attention_desc), ctypes.POINTER(_vp)]),
+    ("cross_attention_destroy", None, [_vp]),
+    ("cross_attention_workspace_size", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    ("cross_attention_get_plan_info", ctypes.c_int, [_vp, ctypes.POINTER(conv2d_plan_info)]),
+    ("cross_attention_forward", ctypes.c_int, [_vp] * 9 + [ctypes.c_size_t, _vp]),
     ("is_lds_tile_bytes", ctypes.c_size_t, [ctypes.c_int] * 6),
     ("is_swizzle_col", ctypes.c_int, [ctypes.c_int] * 5),
     ("is_persistent_grid", ctypes.c_int, [ctypes.c_int, ctypes.c_int]),

@@ -1,0 +1,366 @@
+"""Python binding of the attention operators: rotary positions, the norm of
+queries and keys with the rotation, and cross attention (include/imgstencil.h).
+
+Tensors are torch device tensors n x len x heads x d with a contiguous last
+dimension and any other strides; an fp16 NHWC feature map (n, H, W, C) viewed as
+(n, H * W, heads, C // heads) is one. The functions with the C names marshal
+arguments to the C ABI and nothing else; Rotary and CrossAttention own a plan,
+check their tensors and launch on torch's current stream of the tensors' device.
+"""
+import ctypes
+
+from . import _abi
+from ._abi import cross_attention_desc, conv2d_plan_info, is_tokens, qk_norm_desc, rotary_desc
+
+_LAYOUTS = {"half": _abi.IS_ROTARY_HALF, "interleaved": _abi.IS_ROTARY_INTERLEAVED}
+_SCALINGS = {"none": _abi.IS_ROTARY_UNSCALED, "linear": _abi.IS_ROTARY_LINEAR, "ntk": _abi.IS_ROTARY_NTK,
+             "ramp": _abi.IS_ROTARY_RAMP}
+_NORMS = {"rms": _abi.IS_NORM_RMS, "layer": _abi.IS_NORM_LAYER}
+
+
+# ------------------------------------------------------------------ the C names
+def rotary_create(desc):
+    """Returns an opaque plan handle (int); raises ImgStencilError on a bad desc."""
+    plan = ctypes.c_void_p()
+    _abi.check(_abi.load().rotary_create(ctypes.byref(desc), ctypes.byref(plan)), "rotary_create")
+    return plan.value
+
+
+def rotary_destroy(plan):
+    _abi.load().rotary_destroy(plan)
+
+
+def rotary_get_frequencies(plan):
+    """The frequencies of one axis after scaling (radians per position)."""
+    n = ctypes.c_int()
+    arr = (ctypes.c_double * (_abi.IS_MAX_HEAD_DIM // 2))()
+    _abi.check(_abi.load().rotary_get_frequencies(plan, arr, len(arr), ctypes.byref(n)), "rotary_get_frequencies")
+    return list(arr[:n.value])
+
+
+def rotary_forward(plan, dtype, xt, x_ptr, pos_ptr, pos_batch_stride, yt, y_ptr, stream):
+    """xt, yt: is_tokens; raw pointers (ints) and a hipStream_t (int)."""
+    _abi.check(_abi.load().rotary_forward(plan, dtype, xt, x_ptr, pos_ptr or None, pos_batch_stride, yt, y_ptr,
+                                          stream or None), "rotary_forward")
+
+
+def qk_norm_rotary_forward(plan, desc, q_ptr, k_ptr, q_weight_ptr, k_weight_ptr, q_pos_ptr, k_pos_ptr, q_out_ptr,
+                           k_out_ptr, stream):
+    _abi.check(_abi.load().qk_norm_rotary_forward(plan, ctypes.byref(desc), q_ptr or None, k_ptr or None,
+                                                  q_weight_ptr or None, k_weight_ptr or None, q_pos_ptr or None,
+                                                  k_pos_ptr or None, q_out_ptr or None, k_out_ptr or None,
+                                                  stream or None), "qk_norm_rotary_forward")
+
+
+def cross_attention_create(desc):
+    plan = ctypes.c_void_p()
+    _abi.check(_abi.load().cross_attention_create(ctypes.byref(desc), ctypes.byref(plan)), "cross_attention_create")
+    return plan.value
+
+
+def cross_attention_destroy(plan):
+    _abi.load().cross_attention_destroy(plan)
+
+
+def cross_attention_workspace_size(plan):
+    n = ctypes.c_size_t()
+    _abi.check(_abi.load().cross_attention_workspace_size(plan, ctypes.byref(n)), "cross_attention_workspace_size")
+    return n.value
+
+
+def cross_attention_get_plan_info(plan):
+    """grid: (row tiles over all heads and entries, parts of the keys, 1); tile:
+    (keys per part, rows per workgroup)."""
+    info = conv2d_plan_info()
+    _abi.check(_abi.load().cross_attention_get_plan_info(plan, ctypes.byref(info)), "cross_attention_get_plan_info")
+    return {"kernel": info.kernel.decode(), "grid": (info.grid_x, info.grid_y, info.grid_z), "block": info.block,
+            "lds_bytes": info.lds_bytes, "tile": (info.tile_w, info.tile_h), "flops": info.flops,
+            "bytes": info.bytes}
+
+
+def cross_attention_forward(plan, q_ptr, k_ptr, v_ptr, mask_ptr, lengths_ptr, out_ptr, lse_ptr, ws_ptr, ws_bytes,
+                            stream):
+    _abi.check(_abi.load().cross_attention_forward(plan, q_ptr or None, k_ptr or None, v_ptr or None, mask_ptr or None,
+                                                   lengths_ptr or None, out_ptr or None, lse_ptr or None,
+                                                   ws_ptr or None, ws_bytes, stream or None),
+               "cross_attention_forward")
+
+
+# ---------------------------------------------------------------- torch helpers
+def _dtype(t, name, f32=True):
+    import torch
+    known = {torch.float16: _abi.IS_F16, torch.bfloat16: _abi.IS_BF16}
+    if f32:
+        known[torch.float32] = _abi.IS_F32
+    if not isinstance(t, torch.Tensor) or t.dtype not in known:
+        raise TypeError("%s must be a %sfloat16 or bfloat16 tensor" % (name, "float32, " if f32 else ""))
+    return known[t.dtype]
+
+
+# Shape, dtype and stride checks come before the device checks, so that every
+# rejected argument is reported the same way with or without a GPU.
+def _check_tokens(t, name, dtype, d=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError("%s must be a %s tensor" % (name, dtype))
+    if t.dim() != 4:
+        raise ValueError("%s must be n x len x heads x d, got shape %s" % (name, tuple(t.shape)))
+    if d is not None and t.shape[3] != d:
+        raise ValueError("%s has %d elements per head, expected %d" % (name, t.shape[3], d))
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+
+
+def _check_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != device):
+            raise TypeError("%s must be a tensor on %s" % (name, device if device.type == "cuda" else "a GPU"))
+
+
+def _tokens(t):
+    n, length, heads, _ = t.shape
+    s = t.stride()
+    return is_tokens(n, length, heads, s[0], s[1], s[2])
+
+
+def _check_positions(pos, t, axes, name):
+    """int32, (n or 1) x len x axes, or (n or 1) x len for one axis; returns the
+    batch stride in elements (0: one row set for the whole batch)."""
+    import torch
+    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32:
+        raise TypeError("%s must be an int32 tensor" % name)
+    shape = tuple(pos.shape) + ((1,) if pos.dim() == 2 and axes == 1 else ())
+    if len(shape) != 3 or shape[0] not in (1, t.shape[0]) or shape[1] != t.shape[1] or shape[2] != axes:
+        raise ValueError("%s must be %d (or 1) x %d x %d, got shape %s" % (name, t.shape[0], t.shape[1], axes,
+                                                                          tuple(pos.shape)))
+    if not pos[:1].is_contiguous():
+        raise ValueError("%s must have contiguous rows" % name)
+    return 0 if shape[0] == 1 else pos.stride(0)
+
+
+def _check_weight(w, d, name):
+    import torch
+    if w is None:
+        return
+    if not isinstance(w, torch.Tensor) or w.dtype != torch.float32:
+        raise TypeError("%s must be a float32 tensor" % name)
+    if tuple(w.shape) != (d,) or not w.is_contiguous():
+        raise ValueError("%s must hold %d contiguous values, got shape %s" % (name, d, tuple(w.shape)))
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(t, stream):
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+
+
+class Rotary:
+    """Rotary positions for heads of d elements, the first `rot` of which turn
+    (None: all). axes: positions per token (2: row and column of an image);
+    layout "half" or "interleaved"; scaling "none", "linear", "ntk" or "ramp"
+    (see rotary_desc in include/imgstencil.h): factor, and for "ramp" the trained
+    length original_len and ramp = (low, high) in turns over it; magnitude
+    multiplies what turns. Serves tensors of any length, dtype and head count."""
+
+    def __init__(self, d, rot=None, axes=1, layout="half", base=10000.0, scaling="none", factor=1.0,
+                 original_len=0, ramp=(1.0, 32.0), magnitude=1.0):
+        if layout not in _LAYOUTS:
+            raise ValueError("layout must be one of %s" % sorted(_LAYOUTS))
+        if scaling not in _SCALINGS:
+            raise ValueError("scaling must be one of %s" % sorted(_SCALINGS))
+        self.d, self.rot, self.axes = d, d if rot is None else rot, axes
+        desc = rotary_desc(d, self.rot, axes, _LAYOUTS[layout], _SCALINGS[scaling], original_len, base, factor,
+                           ramp[0], ramp[1], magnitude)
+        self.handle = rotary_create(desc)
+        # Bound now: at interpreter exit the module's globals may already be
+        # gone when __del__ runs.
+        self._destroy = _abi.load().rotary_destroy
+
+    def frequencies(self):
+        return rotary_get_frequencies(self.handle)
+
+    def apply(self, x, positions, out=None, stream=None):
+        """x rotated, into `out` (x itself: in place; None: a new dense tensor).
+        positions: int32, (n or 1) x len x axes."""
+        import torch
+        code = _dtype(x, "x")
+        _check_tokens(x, "x", x.dtype, self.d)
+        pb = _check_positions(positions, x, self.axes, "positions")
+        if out is not None:
+            _check_tokens(out, "out", x.dtype, self.d)
+            if out.shape != x.shape:
+                raise ValueError("out has shape %s, x %s" % (tuple(out.shape), tuple(x.shape)))
+        _check_device(x.device, x=x, positions=positions, out=out)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        rotary_forward(self.handle, code, _tokens(x), x.data_ptr(), positions.data_ptr(), pb, _tokens(out),
+                       out.data_ptr(), _stream(x, stream))
+        return out
+
+    def apply_qk_norm(self, q, k, q_positions, k_positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                      norm="rms", q_out=None, k_out=None, stream=None):
+        """The norm ("rms" or "layer") of every head of q and k, times the fp32
+        weights (None: ones), rotated. k_positions None: those of q. Returns
+        (q_out, k_out); pass q and k themselves to work in place."""
+        import torch
+        code = _dtype(q, "q")
+        _check_tokens(q, "q", q.dtype, self.d)
+        _check_tokens(k, "k", q.dtype, self.d)
+        if norm not in _NORMS:
+            raise ValueError("norm must be one of %s" % sorted(_NORMS))
+        if k_positions is None:
+            k_positions = q_positions
+        qb = _check_positions(q_positions, q, self.axes, "q_positions")
+        kb = _check_positions(k_positions, k, self.axes, "k_positions")
+        _check_weight(q_weight, self.d, "q_weight")
+        _check_weight(k_weight, self.d, "k_weight")
+        for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if o is not None:
+                _check_tokens(o, name, q.dtype, self.d)
+                if o.shape != t.shape:
+                    raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape), tuple(t.shape)))
+        _check_device(q.device, q=q, k=k, q_positions=q_positions, k_positions=k_positions, q_weight=q_weight,
+                      k_weight=k_weight, q_out=q_out, k_out=k_out)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        desc = qk_norm_desc(code, _NORMS[norm], eps, _tokens(q), _tokens(k), _tokens(q_out), _tokens(k_out), qb, kb)
+        qk_norm_rotary_forward(self.handle, desc, q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                               q_positions.data_ptr(), k_positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                               _stream(q, stream))
+        return q_out, k_out
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        destroy = getattr(self, "_destroy", None)
+        if h and destroy is not None:
+            destroy(h)
+            self.handle = None
+
+
+def _check_qkv(q, k, v):
+    _check_tokens(q, "q", q.dtype)
+    _check_tokens(k, "k", q.dtype, q.shape[3])
+    _check_tokens(v, "v", q.dtype, q.shape[3])
+    if v.shape != k.shape:
+        raise ValueError("k has shape %s, v %s" % (tuple(k.shape), tuple(v.shape)))
+    if k.shape[0] != q.shape[0]:
+        raise ValueError("q has %d batch entries, k and v %d" % (q.shape[0], k.shape[0]))
+    if k.shape[2] == 0 or q.shape[2] % k.shape[2]:
+        raise ValueError("%d query heads do not share %d key heads evenly" % (q.shape[2], k.shape[2]))
+
+
+class CrossAttention:
+    """The plan of cross attention for tensors laid out like q (n x lq x hq x d),
+    k and v (n x lk x hkv x d) and out (like q; None: dense). Only shapes,
+    strides and dtype are taken from them. scale None: 1 / sqrt(d).
+    forward() launches on torch's current stream."""
+
+    def __init__(self, q, k, v, out=None, scale=None):
+        code = _dtype(q, "q", f32=False)
+        _check_qkv(q, k, v)
+        if out is not None:
+            _check_tokens(out, "out", q.dtype, q.shape[3])
+            if out.shape != q.shape:
+                raise ValueError("out has shape %s, q %s" % (tuple(out.shape), tuple(q.shape)))
+        if scale is not None and scale == 0:
+            raise ValueError("scale must not be 0")
+        n, lq, hq, d = q.shape
+        lk, hkv = k.shape[1], k.shape[2]
+        dense = (lq * hq * d, hq * d, d, 1)
+        self._like = tuple((tuple(t.shape), tuple(t.stride())) for t in (q, k, v)) + (
+            (tuple(q.shape), dense if out is None else tuple(out.stride())),)
+        self.dtype = q.dtype
+        S = ctypes.c_int64 * 3
+        self._desc = cross_attention_desc(n, lq, lk, hq, hkv, d, code, 0.0 if scale is None else scale,
+                                          *[S(*st[:3]) for (_, st) in self._like], lk)
+        self.handle = cross_attention_create(self._desc)
+        self._destroy = _abi.load().cross_attention_destroy
+        self.workspace_bytes = cross_attention_workspace_size(self.handle)
+
+    def info(self):
+        return cross_attention_get_plan_info(self.handle)
+
+    def new_workspace(self, device="cuda"):
+        """A workspace for forward() (None when it needs none). Calls that
+        overlap in time, on different streams, need one each."""
+        import torch
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device) if self.workspace_bytes else None
+
+    def forward(self, q, k, v, out=None, key_mask=None, key_lengths=None, lse=None, workspace=None, stream=None):
+        """Attention into `out` (None: a new dense tensor). key_mask: bool or
+        uint8, n x lk, true where a key is visible; key_lengths: int32, n; lse:
+        float32, n x hq x lq, receives the log-sum-exp of each row. workspace:
+        from new_workspace() (None: allocated for the call)."""
+        import torch
+        for name, t, (shape, stride) in zip(("q", "k", "v", "out"), (q, k, v, out), self._like):
+            if t is None and name == "out":
+                continue
+            if t.dtype != self.dtype:
+                raise TypeError("%s must be a %s tensor" % (name, self.dtype))
+            if t.shape != shape or t.stride() != stride:
+                raise ValueError("%s is %s with strides %s, the plan is for %s with strides %s"
+                                 % (name, tuple(t.shape), t.stride(), shape, stride))
+        n, lq, hq, lk = self._desc.n, self._desc.lq, self._desc.hq, self._desc.lk
+        if key_mask is not None:
+            if key_mask.dtype not in (torch.bool, torch.uint8):
+                raise TypeError("key_mask must be a bool or uint8 tensor")
+            if key_mask.shape != (n, lk) or not key_mask.is_contiguous():
+                raise ValueError("key_mask must be a contiguous %d x %d, got shape %s" % (n, lk, tuple(key_mask.shape)))
+        if key_lengths is not None:
+            if key_lengths.dtype != torch.int32:
+                raise TypeError("key_lengths must be an int32 tensor")
+            if key_lengths.shape != (n,) or not key_lengths.is_contiguous():
+                raise ValueError("key_lengths must hold %d values, got shape %s" % (n, tuple(key_lengths.shape)))
+        if lse is not None:
+            if lse.dtype != torch.float32:
+                raise TypeError("lse must be a float32 tensor")
+            if lse.shape != (n, hq, lq) or not lse.is_contiguous():
+                raise ValueError("lse must be a contiguous %d x %d x %d, got shape %s" % (n, hq, lq, tuple(lse.shape)))
+        if stream is not None and (out is None or (workspace is None and self.workspace_bytes)):
+            raise ValueError("a call on a stream of its own needs out and workspace: memory allocated here belongs "
+                             "to torch's current stream")
+        _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
+                      workspace=workspace)
+        if out is None:
+            out = torch.empty(self._like[3][0], dtype=self.dtype, device=q.device)
+        if workspace is None and self.workspace_bytes:
+            workspace = self.new_workspace(q.device)
+        cross_attention_forward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(key_mask),
+                                _ptr(key_lengths), out.data_ptr(), _ptr(lse), _ptr(workspace),
+                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                _stream(q, stream))
+        return out
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        destroy = getattr(self, "_destroy", None)
+        if h and destroy is not None:
+            destroy(h)
+            self.handle = None
+
+
+def rotary(x, positions, plan, out=None):
+    """x rotated by the Rotary `plan` (see Rotary.apply)."""
+    return plan.apply(x, positions, out=out)
+
+
+def qk_norm_rotary(q, k, q_positions, plan, k_positions=None, q_weight=None, k_weight=None, eps=1e-6, norm="rms"):
+    """Normed and rotated queries and keys (see Rotary.apply_qk_norm)."""
+    return plan.apply_qk_norm(q, k, q_positions, k_positions, q_weight, k_weight, eps, norm)
+
+
+def cross_attention(q, k, v, key_mask=None, key_lengths=None, scale=None, return_lse=False):
+    """softmax(scale * q k^T) v over the visible keys. q: n x lq x hq x d; k, v:
+    n x lk x hkv x d (fp16 or bf16). With return_lse also the n x hq x lq fp32
+    log-sum-exp of the rows."""
+    import torch
+    plan = CrossAttention(q, k, v, scale=scale)
+    lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device) \
+        if return_lse else None
+    out = plan.forward(q, k, v, key_mask=key_mask, key_lengths=key_lengths, lse=lse)
+    return (out, lse) if return_lse else out

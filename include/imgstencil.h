@@ -1,7 +1,10 @@
 /*
  * imgstencil.h -- C ABI of the MI355X (gfx950) direct 2D convolution library.
  *
- * The operation (every entry point below computes it, or a chain of it):
+ * The operation (the conv2d_* and conv_chain_* entry points compute it, or a
+ * chain of it; the attention operators for networks that put attention between
+ * their convolution layers are the rotary_*, qk_norm_rotary_* and
+ * cross_attention_* entry points at the end, with their own conventions there):
  *
  *   y[n,k,i,j] = act( sum_{c,u,v} w[k,c,u,v] * x[n,c,i+u-(R-1)/2,j+v-(S-1)/2] + b[k] )
  *
@@ -16,7 +19,8 @@
  * Efficiency for Convolution Kernels on Kepler GPUs" (arXiv 1705.10591) and the
  * multi-channel case its "general case".
  *
- * Conventions for every entry point:
+ * Conventions for the convolution entry points (the attention operators keep
+ * all of them but the contiguity rule and the in-place rule, see there):
  *  - Tensors are caller-owned DEVICE memory, dense and contiguous, with the
  *    base address aligned to 16 bytes (else IS_ERR_MISALIGNED). The library
  *    never allocates device memory on a forward call and keeps no pointer
@@ -58,7 +62,11 @@ typedef enum {
   IS_ERR_WORKSPACE = 6      /* workspace missing or smaller than required */
 } is_status;
 
-typedef enum { IS_F32 = 0, IS_F16 = 1 } is_dtype;
+typedef enum {
+  IS_F32 = 0,
+  IS_F16 = 1,
+  IS_BF16 = 2               /* attention operators only: the convolutions answer IS_ERR_UNSUPPORTED */
+} is_dtype;
 typedef enum { IS_NCHW = 0, IS_NHWC = 1 } is_layout;
 
 /* One convolution layer.
@@ -290,6 +298,173 @@ is_status conv_chain_forward_noalloc(const conv_chain_desc *d, const void *x,
  * launch, "layer_by_layer" otherwise; stencil pipelines: see
  * conv_chain_groups), copied into name[0..len-1]. */
 is_status conv_chain_kernel_name(const conv_chain_desc *d, char *name, size_t len);
+
+/* ------------------------------------------------------------------------
+ * Attention operators on feature maps.
+ *
+ * A token tensor is n x len x heads x d elements. An fp16 NHWC feature map of
+ * the layers above is one without a copy: len = H * W tokens, heads * d = C.
+ * The d elements of a head are contiguous; the batch, token and head strides
+ * are free (in elements, >= 0; 0 repeats an input's data, e.g. one prompt for
+ * a whole batch), so slices of a packed q/k/v projection are taken as they
+ * are. Outputs: no two elements at one address (IS_ERR_INVALID_ARG).
+ * Bases are 16-byte aligned (IS_ERR_MISALIGNED). Data may be IS_F32, IS_F16 or
+ * IS_BF16 where an entry point says so; every sum, norm, angle and softmax
+ * statistic is held in 32 bits or more, and a result is rounded once, to
+ * nearest even. Nothing is cleared by memset and nothing is allocated: every
+ * call may be captured into a HIP graph. Inference only: like the layers
+ * above, the operators have no gradient.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int n, len, heads;                                /* any may be 0: no work */
+  int64_t batch_stride, token_stride, head_stride;  /* elements */
+} is_tokens;
+
+/* Rotary positions. The first `rot` elements of a head are P = rot / 2 pairs,
+ * split evenly over `axes` position axes (1: a sequence; 2: row and column of
+ * an image; 3: with a frame number), Pa = P / axes pairs each. Pair p of a
+ * token at positions pos[0 .. axes-1] turns by the angle
+ *     a = pos[p / Pa] * f[p % Pa],    f[i] = base^(-i / Pa),
+ *     (u, v) -> magnitude * (u cos a - v sin a, u sin a + v cos a).
+ * Elements from rot on pass through (not scaled by magnitude).
+ *  IS_ROTARY_HALF:        pair p is the elements p and p + P
+ *  IS_ROTARY_INTERLEAVED: pair p is the elements 2p and 2p + 1
+ * Scaling for contexts longer than the trained one, by `factor` >= 1:
+ *  IS_ROTARY_LINEAR: f / factor (positions squeezed)
+ *  IS_ROTARY_NTK:    base * factor^(Pa / (Pa - 1)) in place of base, which keeps
+ *                    the fastest pair and slows the slowest by factor (Pa >= 2)
+ *  IS_ROTARY_RAMP:   by the turns r = original_len * f / 2 pi that a pair makes over
+ *                    the trained length: g = clamp((r - ramp_low) / (ramp_high -
+ *                    ramp_low), 0, 1), f g + (f / factor) (1 - g): pairs that turn
+ *                    often stay, slow ones are squeezed (the by-parts
+ *                    interpolation of YaRN, arXiv 2309.00071, section 3.2, whose
+ *                    attention temperature is magnitude = 0.1 ln(factor) + 1)
+ * Angles are formed in 64 bits, so far positions lose nothing: fp32 outputs are
+ * within a few 2^-24 of |x|, 16-bit outputs within their own rounding plus 2^-20. */
+typedef enum { IS_ROTARY_HALF = 0, IS_ROTARY_INTERLEAVED = 1 } is_rotary_layout;
+typedef enum {
+  IS_ROTARY_UNSCALED = 0,
+  IS_ROTARY_LINEAR = 1,
+  IS_ROTARY_NTK = 2,
+  IS_ROTARY_RAMP = 3
+} is_rotary_scaling;
+
+#define IS_MAX_HEAD_DIM 256
+
+typedef struct {
+  int d;                   /* elements of a head, 1 .. IS_MAX_HEAD_DIM */
+  int rot;                 /* leading elements that turn: even, 0 .. d, rot / 2 divisible by axes */
+  int axes;                /* positions per token, 1 .. 3 */
+  is_rotary_layout layout;
+  is_rotary_scaling scaling;
+  int original_len;        /* IS_ROTARY_RAMP: trained length, >= 1 */
+  double base;             /* > 0, finite */
+  double factor;           /* >= 1, finite (ignored when unscaled) */
+  double ramp_low, ramp_high;   /* IS_ROTARY_RAMP: turns, 0 <= low < high */
+  double magnitude;        /* > 0, finite; 1 for none */
+} rotary_desc;
+
+typedef struct rotary_plan_s *rotary_plan;
+
+/* Check a descriptor and compute its frequencies. Host only. The plan is
+ * immutable, serves any number of tokens and may be shared by threads and
+ * streams. Errors: IS_ERR_INVALID_ARG, IS_ERR_UNSUPPORTED (d over
+ * IS_MAX_HEAD_DIM, axes over 3, NTK with one pair per axis), IS_ERR_NO_MEMORY. */
+is_status rotary_create(const rotary_desc *d, rotary_plan *out);
+void rotary_destroy(rotary_plan plan);
+
+/* The Pa frequencies of an axis after scaling, in radians per position:
+ * *count receives Pa and the first min(max, Pa) are written to f. */
+is_status rotary_get_frequencies(rotary_plan plan, double *f, int max, int *count);
+
+/* y = rotated x.
+ *  dtype    : IS_F32, IS_F16 or IS_BF16 (x and y)
+ *  xt, yt   : the two token tensors' sizes (equal) and strides
+ *  positions: int32, [n][len][axes]: an entry's rows are contiguous and start
+ *             pos_batch_stride elements apart (0: one set for the whole batch);
+ *             4-byte aligned; any value. May be NULL when rot is 0.
+ * y may be x itself with the same strides (in place); otherwise the address
+ * ranges must not intersect (IS_ERR_INVALID_ARG). */
+is_status rotary_forward(rotary_plan plan, is_dtype dtype, const is_tokens *xt, const void *x,
+                         const int32_t *positions, int64_t pos_batch_stride, const is_tokens *yt, void *y,
+                         hipStream_t stream);
+
+/* The norm of every head of queries and keys, and the rotation, in one pass and
+ * one launch: y = rotate(norm(x) * w), for q with q_weight and q_positions and
+ * for k with k_weight and k_positions. q and k may have different lengths and
+ * head counts (k->heads shared key heads; k of another frame).
+ *  IS_NORM_RMS  : norm(x) = x / sqrt(mean(x^2) + eps) over the d elements
+ *  IS_NORM_LAYER: norm(x) = (x - mean) / sqrt(mean((x - mean)^2) + eps)
+ * Weights are d fp32 values (16-byte aligned) or NULL for ones; eps >= 0,
+ * finite. Position arguments, dtypes and the in-place rule as in
+ * rotary_forward, for (q, q_out) and (k, k_out); the outputs must not touch
+ * the other input's elements. Either tensor may be empty. */
+typedef enum { IS_NORM_RMS = 1, IS_NORM_LAYER = 2 } is_norm;
+
+typedef struct {
+  is_dtype dtype;
+  is_norm norm;
+  float eps;
+  is_tokens q, k, q_out, k_out;
+  int64_t q_pos_batch_stride, k_pos_batch_stride;
+} qk_norm_desc;
+
+is_status qk_norm_rotary_forward(rotary_plan plan, const qk_norm_desc *d, const void *q, const void *k,
+                                 const float *q_weight, const float *k_weight, const int32_t *q_positions,
+                                 const int32_t *k_positions, void *q_out, void *k_out, hipStream_t stream);
+
+/* Cross attention: queries over an encoder's states of another length,
+ *     out[b,i,h] = sum_j p_j v[b,j,h'],  p = softmax_j(scale * q[b,i,h] . k[b,j,h']),
+ * over the keys j that are visible, with h' = h / (hq / hkv): query heads share
+ * key heads in groups. Key j of entry b is visible when j < key_lengths[b] (if
+ * given; clamped to 0 .. lk) and key_mask[b * mask_batch_stride + j] != 0 (if
+ * given). What k and v hold at keys that are not visible (infinities and NaN
+ * too) has no effect. A row without a visible key gives zeros and lse = -inf.
+ *  n, lq, lk, hq, hkv, d: sizes; n, lq and lk may be 0; hq % hkv == 0; d a
+ *               multiple of 8, 8 .. IS_MAX_HEAD_DIM
+ *  dtype      : IS_F16 or IS_BF16 (q, k, v and out)
+ *  scale      : the score factor, finite; 0 stands for 1 / sqrt(d)
+ *  q, k, v, out strides: batch, token, head in elements, multiples of 8
+ *               (IS_ERR_MISALIGNED), token strides of k and v at most 2^23
+ * The scores' products are fp32 sums of 16-bit products; the softmax is fp32;
+ * p is rounded to the data type for the second product, its sum is not. */
+typedef struct {
+  int n, lq, lk, hq, hkv, d;
+  is_dtype dtype;
+  float scale;
+  int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];
+  int64_t mask_batch_stride;    /* bytes; 0: one mask for the whole batch */
+} cross_attention_desc;
+
+typedef struct cross_attention_plan_s *cross_attention_plan;
+
+/* Check a descriptor and choose a kernel. Host only; immutable, shared by
+ * threads and streams. Errors: IS_ERR_INVALID_ARG, IS_ERR_UNSUPPORTED (dtype,
+ * d, sizes beyond 2^31 workgroups, strides beyond the limits),
+ * IS_ERR_MISALIGNED (strides), IS_ERR_NO_MEMORY. */
+is_status cross_attention_create(const cross_attention_desc *d, cross_attention_plan *out);
+void cross_attention_destroy(cross_attention_plan plan);
+
+/* Device bytes of workspace a forward needs: 0 unless few queries meet many
+ * keys, where the keys are split over workgroups and the parts joined. */
+is_status cross_attention_workspace_size(cross_attention_plan plan, size_t *bytes);
+
+/* What the plan launches (flops and bytes: every key visible). */
+is_status cross_attention_get_plan_info(cross_attention_plan plan, conv2d_plan_info *info);
+
+/* Enqueue on `stream`.
+ *  key_mask   : bytes as above, or NULL; key_lengths: n int32, or NULL
+ *  lse        : NULL, or n x hq x lq fp32 (contiguous): log sum_j exp(score_j) of
+ *               each row, with which results over several sets of keys are joined
+ *  workspace  : cross_attention_workspace_size bytes, 16-byte aligned (NULL if 0);
+ *               its content need not be kept or cleared. Two calls that overlap in
+ *               time need two workspaces.
+ * q, k, v may be NULL when they have no element. out, lse and workspace must
+ * not overlap the inputs or each other (IS_ERR_INVALID_ARG).
+ * Errors: also IS_ERR_MISALIGNED, IS_ERR_WORKSPACE, IS_ERR_HIP. */
+is_status cross_attention_forward(cross_attention_plan plan, const void *q, const void *k, const void *v,
+                                  const uint8_t *key_mask, const int32_t *key_lengths, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* LDS bytes of an input tile that covers tile_w x tile_h outputs of a filter
  * r x s over `channels` channels of `elem_bytes` each: the tile plus its halo,
