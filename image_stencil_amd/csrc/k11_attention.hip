@@ -1,6 +1,32 @@
-// k11_attention.hip -- cross attention, the plain kernel: one workgroup per
-// query row walks the visible keys in tiles of 256 with a running maximum and
-// sum of the softmax.
+// k11_attention.hip -- cross attention on the matrix cores.
+//
+//   out = softmax(scale q k^T) v, one pass over the keys with a running maximum
+//   and sum: with s = q . k, c = |scale| log2(e) (the sign goes into q) and M the
+//   running maximum of c s,  p = 2^(c s - M),  l = sum p,  O = sum p v,  out = O / l.
+//
+// Both products run as v_mfma_f32_32x32x16 with the queries as columns:
+//   S^T (keys x queries) = K Q^T      A = K rows (LDS), B = Q (registers)
+//   O^T (d x queries)    = V^T P^T    A = V columns (transposing LDS reads), B = P
+// The accumulator of S^T puts keys 8 a + 4 h + (0..3) of a query's 32 into lane
+// half h (a = 0..3). The order of a product's inner index is free, so P goes
+// from these registers into the second product as it lies, and V's columns are
+// read in the same order of keys: P never crosses lanes or LDS. M, l and the
+// factor of a rescale belong to a query, which is a lane.
+//
+// A workgroup of NW waves either shares key tiles of KT keys, 32 QB query rows
+// per wave (SHARED: many queries), or lets every wave walk key tiles of its own
+// for the same 32 rows and joins the waves' results at the end (few queries,
+// where the read of k and v is all the work). K and V arrive by LDS DMA in two
+// buffers each, without passing registers. Step j issues K tile j + 2 and V tile
+// j + 1, computes the scores of tile j + 1 beside the exponentials of tile j
+// (matrix cores beside vector unit), then adds tile j's p v beside the maximum
+// of tile j + 1. M moves only when a row's maximum outgrows it by 2^8, so that
+// most steps scale nothing; p stays under 2^8, exact in what follows.
+//
+// Rows of k and v that may not be seen are never fetched (an out-of-range
+// offset makes the DMA write zeros); their scores start from -infinity, in the
+// accumulator (MASK) or after the product (the last tile's end).
+#include <float.h>
 #include <math.h>
 
 #include "attention.hpp"
@@ -9,7 +35,12 @@
 namespace is {
 namespace {
 
-constexpr int kKeys = 256;
+constexpr unsigned kOob = 0xFFFFFFF0u;
+constexpr float kLazy = 8.f;   // log2 of how far a row's maximum may outgrow M
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
 
 struct Args {
   const void *q, *k, *v;
@@ -17,90 +48,584 @@ struct Args {
   const int32_t *lengths;
   void *out;
   float *lse;
-  cross_attention_desc d;
-  float scale;
+  float *part;            // splits > 1: O / l of every block, [block][tile row][d]
+  float *part_lse;        // and M + log2 l, [block][tile row]
+  int64_t qs[3], ks[3], vs[3], os[3], mask_bs;
+  int lq, lk, hq, hkv, d, group, rows, row_tiles, splits, split_keys, groups;
+  unsigned flip;          // sign bits of a negative scale
+  float c;                // |scale| log2(e)
 };
 
-__device__ __forceinline__ float block_max(float v, float *tmp) {
-  for (int i = 32; i; i >>= 1) v = fmaxf(v, __shfl_xor(v, i));
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x / 64] = v;
-  __syncthreads();
-  v = fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3]));
-  __syncthreads();
-  return v;
+// Row pitch of an LDS tile, in 16-byte chunks: a power of two.
+constexpr int chunk_pitch(int dp) { return dp <= 32 ? 4 : dp <= 64 ? 8 : dp <= 128 ? 16 : 32; }
+
+// Chunk c of row r lies in slot c ^ f(r) of its row. K is read one chunk of 16
+// consecutive rows per pass, V as 4 consecutive rows x 64 bytes: with these f
+// both fall on different banks.
+template <int CP>
+__device__ __forceinline__ int fk(int r) {
+  return CP >= 16 ? r & 15 : CP == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+template <int CP>
+__device__ __forceinline__ int fv(int r) {
+  return CP >= 16 ? (r & 3) << 2 : CP == 8 ? (r & 2) << 1 : 0;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kKeys) void is_k11_attention_plain(const Args a) {
-  __shared__ float q[IS_MAX_HEAD_DIM], p[kKeys], tmp[4];
-  const cross_attention_desc &d = a.d;
-  const int64_t row = blockIdx.x;
-  const int i = (int)(row % d.lq), h = (int)(row / d.lq % d.hq), b = (int)(row / d.lq / d.hq);
-  const int hk = h / (d.hq / d.hkv), t = threadIdx.x;
-  const T *qp = static_cast<const T *>(a.q) + b * d.q_stride[0] + i * d.q_stride[1] + h * d.q_stride[2];
-  const T *kp = static_cast<const T *>(a.k) + b * d.k_stride[0] + hk * d.k_stride[2];
-  const T *vp = static_cast<const T *>(a.v) + b * d.v_stride[0] + hk * d.v_stride[2];
-  T *op = static_cast<T *>(a.out) + b * d.out_stride[0] + i * d.out_stride[1] + h * d.out_stride[2];
-  if (t < d.d) q[t] = (float)qp[t];
-  __syncthreads();
-  int len = d.lk;
-  if (a.lengths) len = min(len, max(0, a.lengths[b]));
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = 0; j0 < len; j0 += kKeys) {
-    const int j = j0 + t;
-    const bool see = j < len && (!a.mask || a.mask[b * d.mask_batch_stride + j]);
-    float s = -INFINITY;
-    if (see) {
-      s = 0.f;
-      for (int c = 0; c < d.d; ++c) s += q[c] * (float)kp[j * d.k_stride[1] + c];
-      s *= a.scale;
-    }
-    const float top = fmaxf(m, block_max(s, tmp));
-    const float base = top == -INFINITY ? 0.f : top;
-    const float shrink = expf(m - base);
-    p[t] = see ? expf(s - base) : -1.f;   // -1: not visible
-    __syncthreads();
-    l *= shrink;
-    o *= shrink;
-    for (int c = 0; c < kKeys; ++c) {
-      if (p[c] < 0.f) continue;
-      l += p[c];
-      if (t < d.d) o += p[c] * (float)vp[(int64_t)(j0 + c) * d.v_stride[1] + t];
-    }
-    m = top;
-    __syncthreads();
+__device__ __forceinline__ floatx16 mma(_Float16 __attribute__((ext_vector_type(8))) a,
+                                        _Float16 __attribute__((ext_vector_type(8))) b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx16 mma(__bf16 __attribute__((ext_vector_type(8))) a,
+                                        __bf16 __attribute__((ext_vector_type(8))) b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The value of the lane 32 away, joined by max or sum.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <int DP, int NW, bool SHARED>
+struct Geo {
+  static constexpr int CP = chunk_pitch(DP);
+  static constexpr int KT = SHARED ? 64 : 32;              // keys of a tile
+  static constexpr int NKB = KT / 32;
+  static constexpr int TILE = KT * CP * 16;                // bytes of a K or V tile
+  static constexpr int LOADERS = SHARED ? NW : 1;          // waves that bring a tile
+  static constexpr int NI = KT * CP / 64 / LOADERS;        // 1 KB DMA operations of a wave and tile
+  static constexpr int RING = 4 * TILE;                    // K, K, V, V
+  static constexpr int JOIN_PITCH = DP + 4;                // floats
+  static constexpr int RINGS = SHARED ? RING : NW * RING;
+  static constexpr int JOIN = SHARED ? 0 : NW * 32 * (JOIN_PITCH + 2) * 4;
+  static constexpr int BIAS = RINGS > JOIN ? RINGS : JOIN;
+  static constexpr int BYTES = BIAS + NW * KT * 4;
+  static constexpr int WAVES = BYTES <= 80 * 1024 && NW == 4 ? 2 : 1;   // per SIMD: two workgroups in a CU's LDS
+  static_assert(NI >= 1 && NI * 64 * LOADERS == KT * CP, "whole DMA operations");
+};
+
+template <typename T, int DP, int QB, int NW, bool SHARED, bool MASK>
+__global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_attention(const Args a) {
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  typedef T T2 __attribute__((ext_vector_type(2)));
+  typedef float F2 __attribute__((ext_vector_type(2)));
+  typedef short S4 __attribute__((ext_vector_type(4)));
+  using G = Geo<DP, NW, SHARED>;
+  constexpr int CP = G::CP, KT = G::KT, NKB = G::NKB, NI = G::NI, KK = DP / 16, MB = DP / 32;
+  constexpr int ROWS = SHARED ? 32 * QB * NW : 32;
+  __shared__ __attribute__((aligned(1024))) char lds[G::BYTES];
+  lds_poison(lds, sizeof(lds));
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n32 = lane & 31, half = lane >> 5;
+
+  // Workgroup -> (entry and key head, split, row tile). Row tiles of a group
+  // read the same keys, so a group stays on one XCD: groups are dealt to the 8
+  // XCDs in turn, or in one run of consecutive tiles where 8 does not divide them.
+  int g, rt;
+  if ((a.groups & 7) == 0) {
+    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    g = (i / a.row_tiles) * 8 + x;
+    rt = i % a.row_tiles;
+  } else {
+    const int i = xcd_remap(blockIdx.x, gridDim.x);
+    g = i / a.row_tiles;
+    rt = i % a.row_tiles;
   }
-  if (t < d.d) op[t] = (T)(l == 0.f ? 0.f : o / l);
-  if (t == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+  const int split = g % a.splits, bh = g / a.splits;
+  const int hk = bh % a.hkv, b = bh / a.hkv;
+  const int row0 = rt * ROWS + (SHARED ? wave * 32 * QB : 0);
+
+  int len = a.lk;
+  if (a.lengths) len = min(len, max(0, a.lengths[b]));
+  const int first = split * a.split_keys;
+  const int keys = max(0, min(len - first, a.split_keys));
+  const int tiles = (keys + KT - 1) / KT;
+  // Tiles of this wave, and the first key of its j-th.
+  const int nt = SHARED ? tiles : (tiles - wave + NW - 1) / NW;
+  auto tile_key = [&](int j) { return (SHARED ? j : j * NW + wave) * KT; };
+
+  // ---- DMA: operation i of a wave brings slots 64 (i LOADERS + wave) + lane.
+  const int ktok = (int)(a.ks[1] * 2), vtok = (int)(a.vs[1] * 2);   // bytes, at most 2^24
+  const char *kbase = static_cast<const char *>(a.k) + (b * a.ks[0] + hk * a.ks[2] + first * a.ks[1]) * 2;
+  const char *vbase = static_cast<const char *>(a.v) + (b * a.vs[0] + hk * a.vs[2] + first * a.vs[1]) * 2;
+  char *ring = lds + (SHARED ? 0 : wave * G::RING);
+  int drow[NI];
+  unsigned koff[NI], voff[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int slot = (i * G::LOADERS + (SHARED ? wave : 0)) * 64 + lane;
+    const int r = slot / CP, kc = slot % CP ^ fk<CP>(r), vc = slot % CP ^ fv<CP>(r);
+    drow[i] = r;
+    koff[i] = kc * 8 < a.d ? (unsigned)(r * ktok + kc * 16) : kOob;
+    voff[i] = vc * 8 < a.d ? (unsigned)(r * vtok + vc * 16) : kOob;
+  }
+  auto issue = [&](const char *base, int tok, const unsigned *off, int key, char *dst, uint64_t bits) {
+    const int left = min(keys - key, KT);   // at least 1
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char *>(base + (int64_t)key * tok), (short)0, (left - 1) * tok + a.d * 2, kBufferFlags);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool see = MASK ? (bits >> drow[i]) & 1 : drow[i] < left;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs,
+          (__attribute__((address_space(3))) void *)(dst + (i * G::LOADERS + (SHARED ? wave : 0)) * 1024), 16,
+          see ? off[i] : kOob, 0, 0, 0);
+    }
+  };
+  auto issue_k = [&](int j, uint64_t bits) {
+    issue(kbase, ktok, koff, tile_key(j), ring + (j & 1) * G::TILE, bits);
+  };
+  auto issue_v = [&](int j, uint64_t bits) {
+    issue(vbase, vtok, voff, tile_key(j), ring + (2 + (j & 1)) * G::TILE, bits);
+  };
+  auto arrived = [&]() {   // this wave's DMA, then (a shared tile) every wave's
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt 0, expcnt 7, lgkmcnt 15
+    if constexpr (SHARED) __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+  };
+  // Mask bytes of tile j, one key per lane; 0 past the keys.
+  auto mask_byte = [&](int j) -> int {
+    const int key = tile_key(j) + lane;
+    if (!MASK || lane >= KT || j >= nt || key >= keys) return 0;
+    return a.mask[b * a.mask_bs + first + key];
+  };
+
+  // ---- Queries: B operands, lane = row n32, elements 16 kk + 8 half .. + 7.
+  T8 qf[QB][KK];
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    const int r = row0 + qb * 32 + n32;
+    const int i = r / a.group, h = hk * a.group + r % a.group;
+    const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uintx4 w = {0, 0, 0, 0};
+      if (r < a.rows && (2 * kk + half) * 8 < a.d) {
+        w = *reinterpret_cast<const uintx4 *>(p + (2 * kk + half) * 8);
+        w ^= a.flip;
+      }
+      qf[qb][kk] = __builtin_bit_cast(T8, w);
+    }
+  }
+
+  // ---- LDS read addresses (bytes in a tile).
+  const int kaddr = n32 * CP * 16 + ((half ^ fk<CP>(n32)) * 16);          // ^ 32 kk
+  const int i16 = lane & 15, vr = 4 * half + (i16 >> 2);
+  const int vaddr = vr * CP * 16 + (((2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ fv<CP>(vr)) * 16) + (i16 & 1) * 8;  // ^ 64 mb
+  float *bias = reinterpret_cast<float *>(lds + G::BIAS) + wave * KT;
+
+  floatx16 s[QB][NKB], o[QB][MB];
+  float m[QB], l[QB];
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    m[qb] = -FLT_MAX;
+    l[qb] = 0.f;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[qb][mb][e] = 0.f;
+  }
+
+  // Scores of tile j (in K buffer j & 1).
+  auto scores = [&](int j, uint64_t bits) {
+    const char *kt = ring + (j & 1) * G::TILE;
+    if constexpr (MASK) {
+      if (lane < KT) bias[lane] = (bits >> lane) & 1 ? 0.f : -INFINITY;
+    }
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+      floatx16 init;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) init[e] = 0.f;
+      if constexpr (MASK) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const floatx4 f = *reinterpret_cast<const floatx4 *>(bias + kb * 32 + 2 * e + 4 * half);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) init[e + u] = f[u];
+        }
+      }
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) s[qb][kb] = init;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const T8 kf = *reinterpret_cast<const T8 *>(kt + kb * 32 * CP * 16 + (kaddr ^ (kk * 32)));
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) s[qb][kb] = mma(kf, qf[qb][kk], s[qb][kb]);
+      }
+    }
+  };
+  // The end of the last tile.
+  auto cut = [&](int j) {
+    if constexpr (!MASK) {
+      const int left = keys - tile_key(j);
+      if (left >= KT) return;
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (kb * 32 + 8 * (e >> 2) + 4 * half + (e & 3) >= left) s[qb][kb][e] = -INFINITY;
+    }
+  };
+  // M of tile j's scores; O and l follow it when it has to move.
+  auto maximum = [&](float *top) {
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      float x = s[qb][0][0];
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x = fmaxf(x, s[qb][kb][e]);
+      top[qb] = max_halves(x) * a.c;
+    }
+  };
+  auto follow = [&](const float *top) {
+    bool grow = false;
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) grow |= top[qb] > m[qb] + kLazy;
+    if (!__any(grow)) return;
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      const float next = fmaxf(m[qb], top[qb]);
+      const float f = __builtin_amdgcn_exp2f(m[qb] - next);
+      m[qb] = next;
+      l[qb] *= f;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[qb][mb][e] *= f;
+    }
+  };
+  T8 pf[QB][NKB][2];
+  // p of the scores, rounded to T for the second product (the matrix cores take
+  // no wider operand); the sum l takes them in 32 bits.
+  auto exponentials = [&]() {
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uintx4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const F2 p = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[qb][kb][8 * t + 2 * e], a.c, -m[qb])),
+                          __builtin_amdgcn_exp2f(__builtin_fmaf(s[qb][kb][8 * t + 2 * e + 1], a.c, -m[qb]))};
+            sum[e] += p[0] + p[1];
+            w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(p, T2));
+          }
+          pf[qb][kb][t] = __builtin_bit_cast(T8, w);
+        }
+      l[qb] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+  };
+  auto product = [&](int j) {
+    const char *vt = ring + (2 + (j & 1)) * G::TILE;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          typedef __attribute__((address_space(3))) S4 *P;
+          const char *p = vt + (32 * kb + 16 * t) * CP * 16 + (vaddr ^ (mb * 64));
+          const S4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+          const S4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 8 * CP * 16));
+          const T8 vf = __builtin_bit_cast(T8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) o[qb][mb] = mma(vf, pf[qb][kb][t], o[qb][mb]);
+        }
+  };
+
+  if (nt > 0) {
+    float top[QB];
+    uint64_t bits1 = 0;
+    int next = 0;
+    const uint64_t bits0 = __ballot(mask_byte(0) != 0);
+    bits1 = __ballot(mask_byte(1) != 0);
+    next = mask_byte(2);
+    issue_k(0, bits0);
+    arrived();
+    issue_v(0, bits0);
+    if (nt > 1) issue_k(1, bits1);
+    scores(0, bits0);
+    cut(0);
+    maximum(top);
+    follow(top);
+    for (int j = 0; j + 1 < nt; ++j) {
+      arrived();
+      const uint64_t bits2 = __ballot(next != 0);
+      next = mask_byte(j + 3);
+      issue_v(j + 1, bits1);
+      if (j + 2 < nt) issue_k(j + 2, bits2);
+      exponentials();
+      scores(j + 1, bits1);
+      product(j);
+      cut(j + 1);
+      maximum(top);
+      follow(top);
+      bits1 = bits2;
+    }
+    arrived();
+    exponentials();
+    product(nt - 1);
+  }
+
+  // ---- Results: lane = row n32, elements 32 mb + 8 a + 4 half + (0..3) of o.
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) l[qb] = sum_halves(l[qb]);
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      const int tr = wave * 32 * QB + qb * 32 + n32, r = rt * ROWS + tr;
+      const float inv = l[qb] == 0.f ? 0.f : 1.f / l[qb];
+      if (a.splits > 1) {
+        const int64_t at = ((int64_t)g * a.row_tiles + rt) * ROWS + tr;
+        if (r < a.rows) {
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int e = 32 * mb + 8 * u + 4 * half;
+              if (e < a.d) {
+                floatx4 f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] = o[qb][mb][4 * u + x] * inv;
+                *reinterpret_cast<floatx4 *>(a.part + at * a.d + e) = f;
+              }
+            }
+          if (half == 0) a.part_lse[at] = l[qb] == 0.f ? -INFINITY : m[qb] + __log2f(l[qb]);
+        }
+      } else {
+        const int i = r / a.group, h = hk * a.group + r % a.group;
+        T *p = static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int u = 0; u < 4; u += 2) {
+            // Halves of 8 elements lie in the two lane halves: swap, so that lane
+            // half h has all of chunk u + h.
+            unsigned w[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const F2 f = {o[qb][mb][4 * (u + x) + 2 * y] * inv, o[qb][mb][4 * (u + x) + 2 * y + 1] * inv};
+                w[x][y] = __builtin_bit_cast(unsigned, __builtin_convertvector(f, T2));
+              }
+            const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+            const int e = 32 * mb + 8 * (u + half);
+            if (r < a.rows && e < a.d) *reinterpret_cast<uintx4 *>(p + e) = uintx4{s0[0], s1[0], s0[1], s1[1]};
+          }
+        if (a.lse && r < a.rows && half == 0)
+          a.lse[((int64_t)b * a.hq + h) * a.lq + i] =
+              l[qb] == 0.f ? -INFINITY : (m[qb] + __log2f(l[qb])) * 0.69314718055994531f;
+      }
+    }
+  } else {
+    // Join the waves: out = sum_w 2^(M_w - M) O_w / sum_w 2^(M_w - M) l_w.
+    float *jo = reinterpret_cast<float *>(lds), *jm = jo + NW * 32 * G::JOIN_PITCH, *jl = jm + NW * 32;
+    __syncthreads();
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        floatx4 f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[x] = o[0][mb][4 * u + x];
+        *reinterpret_cast<floatx4 *>(jo + (wave * 32 + n32) * G::JOIN_PITCH + 32 * mb + 8 * u + 4 * half) = f;
+      }
+    if (half == 0) {
+      jm[wave * 32 + n32] = m[0];
+      jl[wave * 32 + n32] = l[0];
+    }
+    __syncthreads();
+    const int chunks = a.d / 8;
+    for (int it = threadIdx.x; it < 32 * chunks; it += NW * 64) {
+      const int tr = it / chunks, e = (it % chunks) * 8, r = rt * ROWS + tr;
+      if (r >= a.rows) break;   // rows only grow with it
+      float top = jm[tr], sum = 0.f, f[8] = {};
+#pragma unroll
+      for (int w = 1; w < NW; ++w) top = fmaxf(top, jm[w * 32 + tr]);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float x = __builtin_amdgcn_exp2f(jm[w * 32 + tr] - top);
+        sum += x * jl[w * 32 + tr];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) f[y] += x * jo[(w * 32 + tr) * G::JOIN_PITCH + e + y];
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse2 = sum == 0.f ? -INFINITY : top + __log2f(sum);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) f[y] *= inv;
+      if (a.splits > 1) {
+        const int64_t at = ((int64_t)g * a.row_tiles + rt) * ROWS + tr;
+        floatx4 *p = reinterpret_cast<floatx4 *>(a.part + at * a.d + e);
+        p[0] = floatx4{f[0], f[1], f[2], f[3]};
+        p[1] = floatx4{f[4], f[5], f[6], f[7]};
+        if (e == 0) a.part_lse[at] = lse2;
+      } else {
+        const int i = r / a.group, h = hk * a.group + r % a.group;
+        T8 w;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = (T)f[y];
+        *reinterpret_cast<T8 *>(static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2] + e) = w;
+        if (a.lse && e == 0) a.lse[((int64_t)b * a.hq + h) * a.lq + i] = lse2 * 0.69314718055994531f;
+      }
+    }
+  }
+}
+
+// Joins the splits of a row: a thread takes 8 elements.
+template <typename T>
+__global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int tile_rows, int64_t items) {
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (it >= items) return;
+  const int chunks = a.d / 8, e = (int)(it % chunks) * 8;
+  const int64_t row = it / chunks;
+  const int r = (int)(row % a.rows), bh = (int)(row / a.rows);
+  const int rt = r / tile_rows, tr = r % tile_rows;
+  const int64_t step = (int64_t)a.row_tiles * tile_rows;
+  const int64_t at = ((int64_t)bh * a.splits * a.row_tiles + rt) * tile_rows + tr;
+  float top = -FLT_MAX, sum = 0.f, f[8] = {};
+  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, a.part_lse[at + i * step]);
+  for (int i = 0; i < a.splits; ++i) {
+    const float w = __builtin_amdgcn_exp2f(a.part_lse[at + i * step] - top);
+    const floatx4 *p = reinterpret_cast<const floatx4 *>(a.part + (at + i * step) * a.d + e);
+    const floatx4 x = p[0], y = p[1];
+    sum += w;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f[u] += w * x[u];
+      f[4 + u] += w * y[u];
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T8 w;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) w[u] = (T)(f[u] * inv);
+  const int b = bh / a.hkv, i = r / a.group, h = bh % a.hkv * a.group + r % a.group;
+  *reinterpret_cast<T8 *>(static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2] + e) = w;
+  if (a.lse && e == 0)
+    a.lse[((int64_t)b * a.hq + h) * a.lq + i] =
+        sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+}
+
+constexpr int kHeads[] = {32, 64, 96, 128, 160, 192, 256};   // padded head sizes
+
+// Calls f(std::integral_constant<int, DP>) for the plan's padded head size.
+template <typename F>
+hipError_t for_head(int dp, F &&f) {
+  switch (dp) {
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 96: return f(std::integral_constant<int, 96>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 160: return f(std::integral_constant<int, 160>{});
+    case 192: return f(std::integral_constant<int, 192>{});
+    default: return f(std::integral_constant<int, 256>{});
+  }
+}
+
+constexpr int few_waves(int dp) { return dp <= 128 ? 4 : 2; }
+
+template <typename T>
+hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
+  const unsigned blocks = (unsigned)(p.units * p.splits);
+  hipError_t e = for_head(p.dp, [&](auto dp) -> hipError_t {
+    constexpr int DP = decltype(dp)::value;
+    if (p.tile_rows == 32) {
+      constexpr int NW = few_waves(DP);
+      return a.mask ? launch_kernel(is_k11_attention<T, DP, 1, NW, false, true>, dim3(blocks), dim3(NW * 64), 0, s, a)
+                    : launch_kernel(is_k11_attention<T, DP, 1, NW, false, false>, dim3(blocks), dim3(NW * 64), 0, s, a);
+    }
+    return a.mask ? launch_kernel(is_k11_attention<T, DP, 1, 4, true, true>, dim3(blocks), dim3(256), 0, s, a)
+                  : launch_kernel(is_k11_attention<T, DP, 1, 4, true, false>, dim3(blocks), dim3(256), 0, s, a);
+  });
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t items = (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8);
+  return launch_kernel(is_k11_attention_join<T>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a,
+                       p.tile_rows, items);
 }
 
 }  // namespace
 
 bool configure_attention(AttentionPlan &p) {
   const cross_attention_desc &d = p.d;
-  p.name = "is_k11_attention_plain";
   p.group = d.hq / d.hkv;
   p.rows = d.lq * p.group;
-  p.dp = d.d;
-  p.tile_rows = 1;
-  p.row_tiles = p.rows;
-  p.splits = 1;
-  p.split_keys = d.lk;
-  p.block = kKeys;
-  p.lds = 0;
+  p.dp = kHeads[0];
+  for (const int h : kHeads)
+    if (p.dp < d.d) p.dp = h;
+  const bool few = p.rows <= 32;
+  p.name = few ? "is_k11_attention_few" : "is_k11_attention";
+  p.tile_rows = few ? 32 : 128;
+  p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  p.block = few ? 64 * few_waves(p.dp) : 256;
   p.units = (int64_t)d.n * d.hkv * p.row_tiles;
-  return p.units <= 2147483647;
+  const int tile = few ? 32 * few_waves(p.dp) : 64;
+  const int slots = few ? 256 : 512;
+  const int64_t most = d.lk / (few ? 512 : 256);
+  int64_t splits = p.units > 0 ? slots / p.units : 1;
+  splits = splits < most ? splits : most;
+  splits = splits > 1 ? splits : 1;
+  p.split_keys = (int)(((d.lk + splits - 1) / splits + tile - 1) / tile * tile);
+  if (p.split_keys < tile) p.split_keys = tile;
+  p.splits = (int)((d.lk + (int64_t)p.split_keys - 1) / p.split_keys);
+  if (p.splits < 1) p.splits = 1;
+  return p.units * p.splits <= 2147483647;
 }
 
-size_t attention_workspace(const AttentionPlan &) { return 0; }
+size_t attention_workspace(const AttentionPlan &p) {
+  return p.splits == 1 ? 0 : (size_t)p.units * p.splits * p.tile_rows * (p.d.d + 1) * 4;
+}
 
 hipError_t launch_attention(const AttentionPlan &p, const void *q, const void *k, const void *v,
-                            const uint8_t *mask, const int32_t *lengths, void *out, float *lse, void *,
+                            const uint8_t *mask, const int32_t *lengths, void *out, float *lse, void *ws,
                             hipStream_t s) {
-  const Args a = {q, k, v, mask, lengths, out, lse, p.d, p.scale};
-  if (p.d.dtype == IS_F16)
-    return launch_kernel(is_k11_attention_plain<_Float16>, dim3((unsigned)p.units), dim3(kKeys), 0, s, a);
-  return launch_kernel(is_k11_attention_plain<__bf16>, dim3((unsigned)p.units), dim3(kKeys), 0, s, a);
+  const cross_attention_desc &d = p.d;
+  Args a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.mask = mask;
+  a.lengths = lengths;
+  a.out = out;
+  a.lse = lse;
+  a.part = static_cast<float *>(ws);
+  a.part_lse = a.part ? a.part + (size_t)p.units * p.splits * p.tile_rows * d.d : nullptr;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = d.q_stride[i];
+    a.ks[i] = d.k_stride[i];
+    a.vs[i] = d.v_stride[i];
+    a.os[i] = d.out_stride[i];
+  }
+  a.mask_bs = d.mask_batch_stride;
+  a.lq = d.lq;
+  a.lk = d.lk;
+  a.hq = d.hq;
+  a.hkv = d.hkv;
+  a.d = d.d;
+  a.group = p.group;
+  a.rows = p.rows;
+  a.row_tiles = p.row_tiles;
+  a.splits = p.splits;
+  a.split_keys = p.split_keys;
+  a.groups = d.n * d.hkv * p.splits;
+  a.flip = p.scale < 0.f ? 0x80008000u : 0u;
+  a.c = (float)(fabs((double)p.scale) * 1.4426950408889634);
+  return d.dtype == IS_F16 ? launch_t<_Float16>(p, a, s) : launch_t<__bf16>(p, a, s);
 }
 
 }  // namespace is
