@@ -80,6 +80,18 @@ __device__ __forceinline__ floatx16 mma(__bf16 __attribute__((ext_vector_type(8)
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// 16 bytes per lane from a buffer straight into LDS at dst + 16 lane (zeros for
+// an offset outside the buffer). Written as an instruction because the compiler
+// takes the builtin for a store that any later transposing LDS read may meet,
+// and waits for it there; the kernel's own waits (arrived) are what is needed.
+// It has no output register, so nothing is open while it runs.
+__device__ __forceinline__ void dma16(uintx4 rs, unsigned dst, unsigned off) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :
+                   : "s"(dst), "v"(off), "s"(rs)
+                   : "memory");
+}
+
 // The value of the lane 32 away, joined by max or sum.
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -154,6 +166,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   const char *kbase = static_cast<const char *>(a.k) + (b * a.ks[0] + hk * a.ks[2] + first * a.ks[1]) * 2;
   const char *vbase = static_cast<const char *>(a.v) + (b * a.vs[0] + hk * a.vs[2] + first * a.vs[1]) * 2;
   char *ring = lds + (SHARED ? 0 : wave * G::RING);
+  const unsigned ring_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
   int drow[NI];
   unsigned koff[NI], voff[NI];
 #pragma unroll
@@ -164,24 +177,29 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
     koff[i] = kc * 8 < a.d ? (unsigned)(r * ktok + kc * 16) : kOob;
     voff[i] = vc * 8 < a.d ? (unsigned)(r * vtok + vc * 16) : kOob;
   }
-  auto issue = [&](const char *base, int tok, const unsigned *off, int key, char *dst, uint64_t bits) {
+  auto issue = [&](const char *base, int tok, const unsigned *off, int key, unsigned dst, uint64_t bits) {
     const int left = min(keys - key, KT);   // at least 1
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(base + (int64_t)key * tok), (short)0, (left - 1) * tok + a.d * 2, kBufferFlags);
+    const uint64_t at = (uint64_t)(uintptr_t)base + (uint64_t)((int64_t)key * tok);
+    uintx4 rs = {(unsigned)at, (unsigned)(at >> 32) & 0xffffu, (unsigned)((left - 1) * tok + a.d * 2),
+                       (unsigned)kBufferFlags};
+    // A descriptor that a vector instruction brought to scalar registers needs
+    // five wait states before a load may use it; the compiler counts none for dma16.
+    __asm__ volatile("s_nop 4" : "+s"(rs));
+    auto all = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const bool see = MASK ? (bits >> drow[i]) & 1 : drow[i] < left;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs,
-          (__attribute__((address_space(3))) void *)(dst + (i * G::LOADERS + (SHARED ? wave : 0)) * 1024), 16,
-          see ? off[i] : kOob, 0, 0, 0);
-    }
+      for (int i = 0; i < NI; ++i) {
+        const bool see = decltype(whole)::value || (MASK ? (bits >> drow[i]) & 1 : drow[i] < left);
+        dma16(rs, dst + (unsigned)(i * G::LOADERS + (SHARED ? wave : 0)) * 1024u, see ? off[i] : kOob);
+      }
+    };
+    if (MASK ? !~(bits | (KT == 64 ? 0 : ~(uint64_t)0 << (KT & 63))) : left == KT) all(std::true_type{});
+    else all(std::false_type{});
   };
-  auto issue_k = [&](int j, uint64_t bits) {
-    issue(kbase, ktok, koff, tile_key(j), ring + (j & 1) * G::TILE, bits);
+  auto issue_k = [&](int j, int buffer, uint64_t bits) {
+    issue(kbase, ktok, koff, tile_key(j), ring_at + buffer * G::TILE, bits);
   };
-  auto issue_v = [&](int j, uint64_t bits) {
-    issue(vbase, vtok, voff, tile_key(j), ring + (2 + (j & 1)) * G::TILE, bits);
+  auto issue_v = [&](int j, int buffer, uint64_t bits) {
+    issue(vbase, vtok, voff, tile_key(j), ring_at + (2 + buffer) * G::TILE, bits);
   };
   auto arrived = [&]() {   // this wave's DMA, then (a shared tile) every wave's
     __asm__ volatile("" ::: "memory");
@@ -220,7 +238,8 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   const int vaddr = vr * CP * 16 + (((2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ fv<CP>(vr)) * 16) + (i16 & 1) * 8;  // ^ 64 mb
   float *bias = reinterpret_cast<float *>(lds + G::BIAS) + wave * KT;
 
-  floatx16 s[QB][NKB], o[QB][MB];
+  typedef floatx16 Scores[QB][NKB];
+  floatx16 o[QB][MB];
   float m[QB], l[QB];
 #pragma unroll
   for (int qb = 0; qb < QB; ++qb) {
@@ -232,51 +251,42 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
       for (int e = 0; e < 16; ++e) o[qb][mb][e] = 0.f;
   }
 
-  // Scores of tile j (in K buffer j & 1).
-  auto scores = [&](int j, uint64_t bits) {
-    const char *kt = ring + (j & 1) * G::TILE;
+  // A operands in the order of their use: F_K of a K tile, F_V of a V tile.
+  constexpr int F_K = NKB * KK, F_V = NKB * 2 * MB;
+  auto k_operand = [&](int buffer, int f) -> T8 {
+    const char *p = ring + buffer * G::TILE + (f / KK) * 32 * CP * 16 + (kaddr ^ (f % KK * 32));
+    return *reinterpret_cast<const T8 *>(p);
+  };
+  auto v_operand = [&](int buffer, int f) -> T8 {
+    typedef __attribute__((address_space(3))) S4 *P;
+    const char *p = ring + (2 + buffer) * G::TILE + (f / MB) * 16 * CP * 16 + (vaddr ^ (f % MB * 64));
+    const S4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+    const S4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 8 * CP * 16));
+    return __builtin_bit_cast(T8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  // What the scores of 32 keys start from.
+  auto start = [&](int kb) -> floatx16 {
+    floatx16 init;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) init[e] = 0.f;
+    if constexpr (MASK) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const floatx4 f = *reinterpret_cast<const floatx4 *>(bias + kb * 32 + 2 * e + 4 * half);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) init[e + u] = f[u];
+      }
+    }
+    return init;
+  };
+  auto set_bias = [&](uint64_t bits) {
     if constexpr (MASK) {
       if (lane < KT) bias[lane] = (bits >> lane) & 1 ? 0.f : -INFINITY;
     }
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb) {
-      floatx16 init;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) init[e] = 0.f;
-      if constexpr (MASK) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const floatx4 f = *reinterpret_cast<const floatx4 *>(bias + kb * 32 + 2 * e + 4 * half);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) init[e + u] = f[u];
-        }
-      }
-#pragma unroll
-      for (int qb = 0; qb < QB; ++qb) s[qb][kb] = init;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        const T8 kf = *reinterpret_cast<const T8 *>(kt + kb * 32 * CP * 16 + (kaddr ^ (kk * 32)));
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb) s[qb][kb] = mma(kf, qf[qb][kk], s[qb][kb]);
-      }
-    }
   };
-  // The end of the last tile.
-  auto cut = [&](int j) {
-    if constexpr (!MASK) {
-      const int left = keys - tile_key(j);
-      if (left >= KT) return;
-#pragma unroll
-      for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (kb * 32 + 8 * (e >> 2) + 4 * half + (e & 3) >= left) s[qb][kb][e] = -INFINITY;
-    }
-  };
-  // M of tile j's scores; O and l follow it when it has to move.
-  auto maximum = [&](float *top) {
+  // The largest score of every row, in M's unit; half of the lanes' maximum
+  // (top) comes from the caller.
+  auto maximum = [&](const Scores &s, float *top) {
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb) {
       float x = s[qb][0][0];
@@ -284,13 +294,36 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
       for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) x = fmaxf(x, s[qb][kb][e]);
-      top[qb] = max_halves(x) * a.c;
+      top[qb] = x;
     }
   };
-  auto follow = [&](const float *top) {
-    bool grow = false;
+  // The end of the last tile: keys past it leave, and its maximum is taken again.
+  auto cut = [&](Scores &s, int j, float *top) {
+    if constexpr (!MASK) {
+      const int left = keys - tile_key(j);
+      if (left >= KT) return;
+      const int mine = left - 4 * half;
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) grow |= top[qb] > m[qb] + kLazy;
+      for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            s[qb][kb][e] = kb * 32 + 8 * (e >> 2) + (e & 3) < mine ? s[qb][kb][e] : -INFINITY;
+            __builtin_amdgcn_sched_barrier(0);   // one comparison at a time: 32 at once spill
+          }
+      maximum(s, top);
+    }
+  };
+  // M follows a row's maximum when that outgrows it, and O and l follow M.
+  auto follow = [&](const float *lane_top) {
+    bool grow = false;
+    float top[QB];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      top[qb] = max_halves(lane_top[qb]) * a.c;
+      grow |= top[qb] > m[qb] + kLazy;
+    }
     if (!__any(grow)) return;
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb) {
@@ -304,80 +337,145 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
         for (int e = 0; e < 16; ++e) o[qb][mb][e] *= f;
     }
   };
-  T8 pf[QB][NKB][2];
-  // p of the scores, rounded to T for the second product (the matrix cores take
-  // no wider operand); the sum l takes them in 32 bits.
-  auto exponentials = [&]() {
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uintx4 w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const F2 p = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[qb][kb][8 * t + 2 * e], a.c, -m[qb])),
-                          __builtin_amdgcn_exp2f(__builtin_fmaf(s[qb][kb][8 * t + 2 * e + 1], a.c, -m[qb]))};
-            sum[e] += p[0] + p[1];
-            w[e] = __builtin_bit_cast(unsigned, __builtin_convertvector(p, T2));
-          }
-          pf[qb][kb][t] = __builtin_bit_cast(T8, w);
-        }
-      l[qb] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    }
-  };
-  auto product = [&](int j) {
-    const char *vt = ring + (2 + (j & 1)) * G::TILE;
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          typedef __attribute__((address_space(3))) S4 *P;
-          const char *p = vt + (32 * kb + 16 * t) * CP * 16 + (vaddr ^ (mb * 64));
-          const S4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
-          const S4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 8 * CP * 16));
-          const T8 vf = __builtin_bit_cast(T8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-          for (int qb = 0; qb < QB; ++qb) o[qb][mb] = mma(vf, pf[qb][kb][t], o[qb][mb]);
-        }
+  // Two exponentials: p, rounded to T for the second product (the matrix cores
+  // take no wider operand); the sum l takes them in 32 bits.
+  auto exponentials = [&](float s0, float s1, int qb, float &sum) -> unsigned {
+    const F2 p = {__builtin_amdgcn_exp2f(__builtin_fmaf(s0, a.c, -m[qb])),
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(s1, a.c, -m[qb]))};
+    sum += p[0];
+    sum += p[1];
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(p, T2));
   };
 
+  // One step: scores of the next tile (NEXT: into n, from K buffer 1 - B) beside
+  // the exponentials of s, then s's p v (V buffer B) beside the next maximum.
+  // A slot is one A operand's products and what the vector unit does in their 32
+  // cycles each; the fences keep the order, since a wave issues in order and the
+  // compiler would put each kind in a run of its own. Operands are read kAhead
+  // slots early.
+  auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top) {
+    constexpr int B = decltype(buffer)::value, NEXT = decltype(next)::value;
+    constexpr int FIRST = NEXT ? 0 : F_K, SLOTS = F_K + F_V;
+    constexpr int kAhead = 3;
+    constexpr int PAIRS = NKB * 8, LAST = F_K + F_V - MB;   // the last p must be there at slot LAST
+    T8 op[kAhead + 1];
+    auto fetch = [&](auto f) {
+      constexpr int F = decltype(f)::value;
+      if constexpr (F < F_K) op[F % (kAhead + 1)] = k_operand(1 - B, F);
+      else if constexpr (F < SLOTS) op[F % (kAhead + 1)] = v_operand(B, F - F_K);
+    };
+    uintx4 p[QB][NKB * 2];
+    float sum[QB][2] = {};
+    static_for<kAhead>([&](auto i) { fetch(std::integral_constant<int, FIRST + decltype(i)::value>{}); });
+    if constexpr (!NEXT) {
+      static_for<PAIRS>([&](auto i) {
+        constexpr int P = decltype(i)::value;
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb)
+          p[qb][P / 4][P % 4] = exponentials(s[qb][P / 8][2 * (P % 8)], s[qb][P / 8][2 * (P % 8) + 1], qb, sum[qb][P & 1]);
+      });
+    }
+    static_for<SLOTS - FIRST>([&](auto i) {
+      constexpr int U = FIRST + decltype(i)::value;
+      fetch(std::integral_constant<int, U + kAhead>{});
+      const T8 x = op[U % (kAhead + 1)];
+      if constexpr (U < F_K) {
+        constexpr int kb = U / KK, kk = U % KK;
+        if constexpr (kk == 0) {
+          const floatx16 init = start(kb);
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) n[qb][kb] = init;
+        }
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) n[qb][kb] = mma(x, qf[qb][kk], n[qb][kb]);
+      } else {
+        constexpr int f = (U - F_K) / MB, mb = (U - F_K) % MB;
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) o[qb][mb] = mma(x, __builtin_bit_cast(T8, p[qb][f]), o[qb][mb]);
+      }
+      if constexpr (NEXT) {
+        // Pairs of exponentials: evenly over the slots before LAST.
+        constexpr int P0 = U < LAST ? U * PAIRS / LAST : PAIRS, P1 = U < LAST ? (U + 1) * PAIRS / LAST : PAIRS;
+        static_for<P1 - P0>([&](auto k) {
+          constexpr int P = P0 + decltype(k)::value;
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb)
+            p[qb][P / 4][P % 4] =
+                exponentials(s[qb][P / 8][2 * (P % 8)], s[qb][P / 8][2 * (P % 8) + 1], qb, sum[qb][P & 1]);
+        });
+        // The next scores' maximum: evenly over the V slots but the first.
+        if constexpr (U > F_K) {
+          constexpr int E0 = (U - F_K - 1) * NKB * 16 / (F_V - 1), E1 = (U - F_K) * NKB * 16 / (F_V - 1);
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) {
+            if constexpr (E0 == 0) top[qb] = n[qb][0][0];
+#pragma unroll
+            for (int e = E0; e < E1; ++e) top[qb] = fmaxf(top[qb], n[qb][e / 16][e % 16]);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) l[qb] += sum[qb][0] + sum[qb][1];
+  };
+
+  // Tile j lies in buffers (j + nt - 1) & 1: the last one in 0.
   if (nt > 0) {
+    Scores s0, s1;
     float top[QB];
-    uint64_t bits1 = 0;
-    int next = 0;
+    int j = 0, next = mask_byte(2);
+    uint64_t bits1 = __ballot(mask_byte(1) != 0);
     const uint64_t bits0 = __ballot(mask_byte(0) != 0);
-    bits1 = __ballot(mask_byte(1) != 0);
-    next = mask_byte(2);
-    issue_k(0, bits0);
-    arrived();
-    issue_v(0, bits0);
-    if (nt > 1) issue_k(1, bits1);
-    scores(0, bits0);
-    cut(0);
-    maximum(top);
-    follow(top);
-    for (int j = 0; j + 1 < nt; ++j) {
+    const int odd = (nt - 1) & 1;
+    // Scores of tile j + 1 into n beside the rest of tile j, whose buffers are B.
+    auto advance = [&](auto buffer, const Scores &s, Scores &n) {
+      constexpr int B = decltype(buffer)::value;
       arrived();
       const uint64_t bits2 = __ballot(next != 0);
       next = mask_byte(j + 3);
-      issue_v(j + 1, bits1);
-      if (j + 2 < nt) issue_k(j + 2, bits2);
-      exponentials();
-      scores(j + 1, bits1);
-      product(j);
-      cut(j + 1);
-      maximum(top);
+      issue_v(j + 1, 1 - B, bits1);
+      if (j + 2 < nt) issue_k(j + 2, B, bits2);
+      set_bias(bits1);
+      step(buffer, std::integral_constant<int, 1>{}, s, n, top);
+      cut(n, j + 1, top);
       follow(top);
       bits1 = bits2;
+      ++j;
+    };
+    issue_k(0, odd, bits0);
+    arrived();
+    issue_v(0, odd, bits0);
+    if (nt > 1) issue_k(1, 1 - odd, bits1);
+    set_bias(bits0);
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+      const floatx16 init = start(kb);
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) s0[qb][kb] = init;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const T8 x = k_operand(odd, kb * KK + kk);
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) s0[qb][kb] = mma(x, qf[qb][kk], s0[qb][kb]);
+      }
+    }
+    maximum(s0, top);
+    cut(s0, 0, top);
+    follow(top);
+    if (odd) {
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) s1[qb][kb] = s0[qb][kb];
+      advance(std::integral_constant<int, 1>{}, s1, s0);
+    }
+    while (j + 1 < nt) {
+      advance(std::integral_constant<int, 0>{}, s0, s1);
+      advance(std::integral_constant<int, 1>{}, s1, s0);
     }
     arrived();
-    exponentials();
-    product(nt - 1);
+    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, s0, s1, top);
   }
 
   // ---- Results: lane = row n32, elements 32 mb + 8 a + 4 half + (0..3) of o.
