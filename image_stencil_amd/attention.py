@@ -117,9 +117,10 @@ def _check_device(device, **tensors):
             raise TypeError("%s must be a tensor on %s" % (name, device if device.type == "cuda" else "a GPU"))
 
 
-def _tokens(t):
-    n, length, heads, _ = t.shape
-    s = t.stride()
+def _tokens(t, dense=False):
+    """The token tensor t, or a new dense one of its shape."""
+    n, length, heads, d = t.shape
+    s = (length * heads * d, heads * d, d) if dense else t.stride()
     return is_tokens(n, length, heads, s[0], s[1], s[2])
 
 
@@ -152,9 +153,45 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _sig(t):
+    """What a layout check looks at."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
 def _stream(t, stream):
+    """torch's current stream of t's device as a number. The raw form is asked
+    for directly: building a Stream object costs a microsecond, a quarter of a
+    small call."""
+    if stream is not None:
+        return stream
     import torch
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _one_device(tensors):
+    """True when all tensors that are given lie on one GPU."""
+    d = tensors[0].get_device()
+    if d < 0 or not tensors[0].is_cuda:
+        return False
+    for t in tensors:
+        if t is not None and (t.get_device() != d or not t.is_cuda):
+            return False
+    return True
+
+
+class _Layouts(dict):
+    """Checked layouts of a plan's calls: shapes, strides and dtypes (never
+    addresses) -> the C arguments that follow from them. A call with a layout
+    seen before skips its checks. Few layouts recur in a program; a stray
+    thousand starts over."""
+    LIMIT = 256
+
+    def keep(self, key, value):
+        if len(self) >= self.LIMIT:
+            self.clear()
+        self[key] = value
+        return value
 
 
 class Rotary:
@@ -175,9 +212,12 @@ class Rotary:
         desc = rotary_desc(d, self.rot, axes, _LAYOUTS[layout], _SCALINGS[scaling], original_len, base, factor,
                            ramp[0], ramp[1], magnitude)
         self.handle = rotary_create(desc)
+        self._lib, self._layouts = _abi.load(), _Layouts()
         # Bound now: at interpreter exit the module's globals may already be
         # gone when __del__ runs.
-        self._destroy = _abi.load().rotary_destroy
+        self._destroy = self._lib.rotary_destroy
+        import torch
+        self._torch = torch
 
     def frequencies(self):
         return rotary_get_frequencies(self.handle)
@@ -185,7 +225,25 @@ class Rotary:
     def apply(self, x, positions, out=None, stream=None):
         """x rotated, into `out` (x itself: in place; None: a new dense tensor).
         positions: int32, (n or 1) x len x axes."""
-        import torch
+        try:
+            key = (x.shape, x.stride(), x.dtype, positions.shape, positions.stride(), positions.dtype, _sig(out))
+            call = self._layouts.get(key)
+        except AttributeError:      # not a tensor: the checks say so
+            key = call = None
+        if call is None:
+            call = self._layouts.keep(key, self._check_apply(x, positions, out))
+        if not _one_device((x, positions, out)):
+            _check_device(x.device, x=x, positions=positions, out=out)
+        if out is None:
+            out = self._torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        code, xt, pb, yt = call
+        st = self._lib.rotary_forward(self.handle, code, xt, x.data_ptr(), positions.data_ptr() or None, pb, yt,
+                                      out.data_ptr(), _stream(x, stream) or None)
+        if st:
+            _abi.check(st, "rotary_forward")
+        return out
+
+    def _check_apply(self, x, positions, out):
         code = _dtype(x, "x")
         _check_tokens(x, "x", x.dtype, self.d)
         pb = _check_positions(positions, x, self.axes, "positions")
@@ -193,26 +251,45 @@ class Rotary:
             _check_tokens(out, "out", x.dtype, self.d)
             if out.shape != x.shape:
                 raise ValueError("out has shape %s, x %s" % (tuple(out.shape), tuple(x.shape)))
-        _check_device(x.device, x=x, positions=positions, out=out)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rotary_forward(self.handle, code, _tokens(x), x.data_ptr(), positions.data_ptr(), pb, _tokens(out),
-                       out.data_ptr(), _stream(x, stream))
-        return out
+        return code, _tokens(x), pb, _tokens(x if out is None else out, out is None)
 
     def apply_qk_norm(self, q, k, q_positions, k_positions=None, q_weight=None, k_weight=None, eps=1e-6,
                       norm="rms", q_out=None, k_out=None, stream=None):
         """The norm ("rms" or "layer") of every head of q and k, times the fp32
         weights (None: ones), rotated. k_positions None: those of q. Returns
         (q_out, k_out); pass q and k themselves to work in place."""
-        import torch
+        if k_positions is None:
+            k_positions = q_positions
+        try:
+            key = (_sig(q), _sig(k), _sig(q_positions), _sig(k_positions), _sig(q_weight), _sig(k_weight), eps, norm,
+                   _sig(q_out), _sig(k_out))
+            call = self._layouts.get(key)
+        except (AttributeError, TypeError):     # not a tensor, no number: the checks say so
+            key = call = None
+        if call is None:
+            call = self._layouts.keep(key, self._check_qk_norm(q, k, q_positions, k_positions, q_weight, k_weight, eps,
+                                                               norm, q_out, k_out))
+        if not _one_device((q, k, q_positions, k_positions, q_weight, k_weight, q_out, k_out)):
+            _check_device(q.device, q=q, k=k, q_positions=q_positions, k_positions=k_positions, q_weight=q_weight,
+                          k_weight=k_weight, q_out=q_out, k_out=k_out)
+        if q_out is None:
+            q_out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = self._torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        st = self._lib.qk_norm_rotary_forward(self.handle, call, q.data_ptr() or None, k.data_ptr() or None,
+                                              _ptr(q_weight), _ptr(k_weight), q_positions.data_ptr() or None,
+                                              k_positions.data_ptr() or None, q_out.data_ptr() or None,
+                                              k_out.data_ptr() or None, _stream(q, stream) or None)
+        if st:
+            _abi.check(st, "qk_norm_rotary_forward")
+        return q_out, k_out
+
+    def _check_qk_norm(self, q, k, q_positions, k_positions, q_weight, k_weight, eps, norm, q_out, k_out):
         code = _dtype(q, "q")
         _check_tokens(q, "q", q.dtype, self.d)
         _check_tokens(k, "k", q.dtype, self.d)
         if norm not in _NORMS:
             raise ValueError("norm must be one of %s" % sorted(_NORMS))
-        if k_positions is None:
-            k_positions = q_positions
         qb = _check_positions(q_positions, q, self.axes, "q_positions")
         kb = _check_positions(k_positions, k, self.axes, "k_positions")
         _check_weight(q_weight, self.d, "q_weight")
@@ -222,17 +299,8 @@ class Rotary:
                 _check_tokens(o, name, q.dtype, self.d)
                 if o.shape != t.shape:
                     raise ValueError("%s has shape %s, expected %s" % (name, tuple(o.shape), tuple(t.shape)))
-        _check_device(q.device, q=q, k=k, q_positions=q_positions, k_positions=k_positions, q_weight=q_weight,
-                      k_weight=k_weight, q_out=q_out, k_out=k_out)
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        desc = qk_norm_desc(code, _NORMS[norm], eps, _tokens(q), _tokens(k), _tokens(q_out), _tokens(k_out), qb, kb)
-        qk_norm_rotary_forward(self.handle, desc, q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-                               q_positions.data_ptr(), k_positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                               _stream(q, stream))
-        return q_out, k_out
+        return qk_norm_desc(code, _NORMS[norm], eps, _tokens(q), _tokens(k), _tokens(q if q_out is None else q_out,
+                            q_out is None), _tokens(k if k_out is None else k_out, k_out is None), qb, kb)
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -261,6 +329,8 @@ class CrossAttention:
     forward() launches on torch's current stream."""
 
     def __init__(self, q, k, v, out=None, scale=None):
+        import torch
+        self._torch = torch
         code = _dtype(q, "q", f32=False)
         _check_qkv(q, k, v)
         if out is not None:
@@ -279,7 +349,8 @@ class CrossAttention:
         self._desc = cross_attention_desc(n, lq, lk, hq, hkv, d, code, 0.0 if scale is None else scale,
                                           *[S(*st[:3]) for (_, st) in self._like], lk)
         self.handle = cross_attention_create(self._desc)
-        self._destroy = _abi.load().cross_attention_destroy
+        self._lib, self._layouts = _abi.load(), _Layouts()
+        self._destroy = self._lib.cross_attention_destroy
         self.workspace_bytes = cross_attention_workspace_size(self.handle)
 
     def info(self):
@@ -296,45 +367,59 @@ class CrossAttention:
         uint8, n x lk, true where a key is visible; key_lengths: int32, n; lse:
         float32, n x hq x lq, receives the log-sum-exp of each row. workspace:
         from new_workspace() (None: allocated for the call)."""
-        import torch
+        try:
+            key = (_sig(q), _sig(k), _sig(v), _sig(out), _sig(key_mask), _sig(key_lengths), _sig(lse))
+            seen = self._layouts.get(key)
+        except AttributeError:      # not a tensor: the checks say so
+            key = seen = None
+        if not seen:
+            self._check_forward(q, k, v, out, key_mask, key_lengths, lse)
+            self._layouts.keep(key, True)
+        if stream is not None and (out is None or (workspace is None and self.workspace_bytes)):
+            raise ValueError("a call on a stream of its own needs out and workspace: memory allocated here belongs "
+                             "to torch's current stream")
+        if not _one_device((q, k, v, out, key_mask, key_lengths, lse, workspace)):
+            _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
+                          workspace=workspace)
+        if out is None:
+            out = self._torch.empty(self._like[3][0], dtype=self.dtype, device=q.device)
+        if workspace is None and self.workspace_bytes:
+            workspace = self.new_workspace(q.device)
+        st = self._lib.cross_attention_forward(self.handle, q.data_ptr() or None, k.data_ptr() or None,
+                                               v.data_ptr() or None, _ptr(key_mask), _ptr(key_lengths),
+                                               out.data_ptr() or None, _ptr(lse), _ptr(workspace),
+                                               workspace.numel() * workspace.element_size()
+                                               if workspace is not None else 0, _stream(q, stream) or None)
+        if st:
+            _abi.check(st, "cross_attention_forward")
+        return out
+
+    def _check_forward(self, q, k, v, out, key_mask, key_lengths, lse):
+        torch = self._torch
         for name, t, (shape, stride) in zip(("q", "k", "v", "out"), (q, k, v, out), self._like):
             if t is None and name == "out":
                 continue
-            if t.dtype != self.dtype:
+            if not isinstance(t, torch.Tensor) or t.dtype != self.dtype:
                 raise TypeError("%s must be a %s tensor" % (name, self.dtype))
             if t.shape != shape or t.stride() != stride:
                 raise ValueError("%s is %s with strides %s, the plan is for %s with strides %s"
                                  % (name, tuple(t.shape), t.stride(), shape, stride))
         n, lq, hq, lk = self._desc.n, self._desc.lq, self._desc.hq, self._desc.lk
         if key_mask is not None:
-            if key_mask.dtype not in (torch.bool, torch.uint8):
+            if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
                 raise TypeError("key_mask must be a bool or uint8 tensor")
             if key_mask.shape != (n, lk) or not key_mask.is_contiguous():
                 raise ValueError("key_mask must be a contiguous %d x %d, got shape %s" % (n, lk, tuple(key_mask.shape)))
         if key_lengths is not None:
-            if key_lengths.dtype != torch.int32:
+            if not isinstance(key_lengths, torch.Tensor) or key_lengths.dtype != torch.int32:
                 raise TypeError("key_lengths must be an int32 tensor")
             if key_lengths.shape != (n,) or not key_lengths.is_contiguous():
                 raise ValueError("key_lengths must hold %d values, got shape %s" % (n, tuple(key_lengths.shape)))
         if lse is not None:
-            if lse.dtype != torch.float32:
+            if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32:
                 raise TypeError("lse must be a float32 tensor")
             if lse.shape != (n, hq, lq) or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous %d x %d x %d, got shape %s" % (n, hq, lq, tuple(lse.shape)))
-        if stream is not None and (out is None or (workspace is None and self.workspace_bytes)):
-            raise ValueError("a call on a stream of its own needs out and workspace: memory allocated here belongs "
-                             "to torch's current stream")
-        _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
-                      workspace=workspace)
-        if out is None:
-            out = torch.empty(self._like[3][0], dtype=self.dtype, device=q.device)
-        if workspace is None and self.workspace_bytes:
-            workspace = self.new_workspace(q.device)
-        cross_attention_forward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(key_mask),
-                                _ptr(key_lengths), out.data_ptr(), _ptr(lse), _ptr(workspace),
-                                workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                _stream(q, stream))
-        return out
 
     def __del__(self):
         h = getattr(self, "handle", None)

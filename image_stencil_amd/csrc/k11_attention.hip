@@ -84,13 +84,29 @@ __device__ __forceinline__ floatx16 mma(__bf16 __attribute__((ext_vector_type(8)
 // an offset outside the buffer). Written as an instruction because the compiler
 // takes the builtin for a store that any later transposing LDS read may meet,
 // and waits for it there; the kernel's own waits (arrived) are what is needed.
-// It has no output register, so nothing is open while it runs.
+// It has no output register, so nothing is open while it runs. A descriptor that
+// a vector instruction brought to scalar registers needs five wait states before
+// a load may use it: the move and the s_nop.
 __device__ __forceinline__ void dma16(uintx4 rs, unsigned dst, unsigned off) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                    :
                    : "s"(dst), "v"(off), "s"(rs)
                    : "memory");
 }
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void dma4(uintx4 rs, unsigned dst, unsigned off) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                   :
+                   : "s"(dst), "v"(off), "s"(rs)
+                   : "memory");
+}
+// A buffer descriptor for them.
+__device__ __forceinline__ uintx4 descriptor(uint64_t at, unsigned bytes) {
+  return uintx4{(unsigned)at, (unsigned)(at >> 32) & 0xffffu, bytes, (unsigned)kBufferFlags};
+}
+
+// s_waitcnt operand: at most n vector-memory operations outstanding.
+constexpr int wait_vm(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
 
 // The value of the lane 32 away, joined by max or sum.
 __device__ __forceinline__ float max_halves(float x) {
@@ -102,7 +118,7 @@ __device__ __forceinline__ float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int DP, int NW, bool SHARED>
+template <int DP, int NW, bool SHARED, bool MASK>
 struct Geo {
   static constexpr int CP = chunk_pitch(DP);
   static constexpr int KT = SHARED ? 64 : 32;              // keys of a tile
@@ -114,19 +130,21 @@ struct Geo {
   static constexpr int JOIN_PITCH = DP + 4;                // floats
   static constexpr int RINGS = SHARED ? RING : NW * RING;
   static constexpr int JOIN = SHARED ? 0 : NW * 32 * (JOIN_PITCH + 2) * 4;
-  static constexpr int BIAS = RINGS > JOIN ? RINGS : JOIN;
-  static constexpr int BYTES = BIAS + NW * KT * 4;
+  static constexpr int MASKS = RINGS > JOIN ? RINGS : JOIN;   // a wave's mask bytes, then its bias
+  static constexpr int MASK_SLOT = 256, MASK_SLOTS = 4;
+  static constexpr int MASK_WAVE = MASK_SLOTS * MASK_SLOT + KT * 4;
+  static constexpr int BYTES = MASKS + (MASK ? NW * MASK_WAVE : 0);
   static constexpr int WAVES = BYTES <= 80 * 1024 && NW == 4 ? 2 : 1;   // per SIMD: two workgroups in a CU's LDS
   static_assert(NI >= 1 && NI * 64 * LOADERS == KT * CP, "whole DMA operations");
 };
 
 template <typename T, int DP, int QB, int NW, bool SHARED, bool MASK>
-__global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_attention(const Args a) {
+__global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void is_k11_attention(const Args a) {
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef T T2 __attribute__((ext_vector_type(2)));
   typedef float F2 __attribute__((ext_vector_type(2)));
   typedef short S4 __attribute__((ext_vector_type(4)));
-  using G = Geo<DP, NW, SHARED>;
+  using G = Geo<DP, NW, SHARED, MASK>;
   constexpr int CP = G::CP, KT = G::KT, NKB = G::NKB, NI = G::NI, KK = DP / 16, MB = DP / 32;
   constexpr int ROWS = SHARED ? 32 * QB * NW : 32;
   __shared__ __attribute__((aligned(1024))) char lds[G::BYTES];
@@ -166,7 +184,8 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   const char *kbase = static_cast<const char *>(a.k) + (b * a.ks[0] + hk * a.ks[2] + first * a.ks[1]) * 2;
   const char *vbase = static_cast<const char *>(a.v) + (b * a.vs[0] + hk * a.vs[2] + first * a.vs[1]) * 2;
   char *ring = lds + (SHARED ? 0 : wave * G::RING);
-  const unsigned ring_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)ring;
+  const unsigned lds_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+  const unsigned ring_at = lds_at + (unsigned)(SHARED ? 0 : wave * G::RING);
   int drow[NI];
   unsigned koff[NI], voff[NI];
 #pragma unroll
@@ -177,14 +196,11 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
     koff[i] = kc * 8 < a.d ? (unsigned)(r * ktok + kc * 16) : kOob;
     voff[i] = vc * 8 < a.d ? (unsigned)(r * vtok + vc * 16) : kOob;
   }
+  // Rows of a tile at `key` that may be seen; a tile past the keys gets zeros.
   auto issue = [&](const char *base, int tok, const unsigned *off, int key, unsigned dst, uint64_t bits) {
-    const int left = min(keys - key, KT);   // at least 1
-    const uint64_t at = (uint64_t)(uintptr_t)base + (uint64_t)((int64_t)key * tok);
-    uintx4 rs = {(unsigned)at, (unsigned)(at >> 32) & 0xffffu, (unsigned)((left - 1) * tok + a.d * 2),
-                       (unsigned)kBufferFlags};
-    // A descriptor that a vector instruction brought to scalar registers needs
-    // five wait states before a load may use it; the compiler counts none for dma16.
-    __asm__ volatile("s_nop 4" : "+s"(rs));
+    const int left = min(keys - key, KT);
+    const uintx4 rs = descriptor((uint64_t)(uintptr_t)base + (uint64_t)((int64_t)key * tok),
+                                 left > 0 ? (unsigned)((left - 1) * tok + a.d * 2) : 0u);
     auto all = [&](auto whole) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -201,17 +217,35 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   auto issue_v = [&](int j, int buffer, uint64_t bits) {
     issue(vbase, vtok, voff, tile_key(j), ring_at + (2 + buffer) * G::TILE, bits);
   };
-  auto arrived = [&]() {   // this wave's DMA, then (a shared tile) every wave's
+  // At most N of this wave's DMA operations still out, then (a shared tile)
+  // every wave's.
+  auto arrived = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    static_assert(N < 64, "vmcnt");
     __asm__ volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt 0, expcnt 7, lgkmcnt 15
+    __builtin_amdgcn_s_waitcnt(wait_vm(N));
     if constexpr (SHARED) __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
   };
-  // Mask bytes of tile j, one key per lane; 0 past the keys.
-  auto mask_byte = [&](int j) -> int {
-    const int key = tile_key(j) + lane;
-    if (!MASK || lane >= KT || j >= nt || key >= keys) return 0;
-    return a.mask[b * a.mask_bs + first + key];
+  // Mask bytes of tile j: the words that hold them, into slot j % 4. The words'
+  // other bytes belong to the same aligned word and are dropped (seen).
+  const unsigned masks_at = lds_at + (unsigned)(G::MASKS + wave * G::MASK_WAVE);
+  const uint64_t mask0 = MASK ? (uint64_t)(uintptr_t)a.mask + (uint64_t)(b * a.mask_bs + first) : 0;
+  auto issue_mask = [&](int j) {
+    if constexpr (MASK) {
+      const uint64_t at = mask0 + (uint64_t)tile_key(j);
+      const int left = min(keys - tile_key(j), KT), skip = (int)(at & 3);
+      const uintx4 rs = descriptor(at & ~(uint64_t)3, left > 0 ? (unsigned)((left + skip + 3) & ~3) : 0u);
+      dma4(rs, masks_at + (unsigned)(j % G::MASK_SLOTS) * G::MASK_SLOT, lane * 4u);
+    }
+  };
+  // A bit for every key of tile j that may be seen.
+  auto seen = [&](int j) -> uint64_t {
+    if constexpr (!MASK) return 0;
+    const int key = tile_key(j);
+    const int skip = (int)((mask0 + (uint64_t)key) & 3);
+    const uint8_t byte = lds[G::MASKS + wave * G::MASK_WAVE + j % G::MASK_SLOTS * G::MASK_SLOT + skip + lane % KT];
+    return __ballot(lane < KT && key + lane < keys && byte != 0);
   };
 
   // ---- Queries: B operands, lane = row n32, elements 16 kk + 8 half .. + 7.
@@ -236,7 +270,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   const int kaddr = n32 * CP * 16 + ((half ^ fk<CP>(n32)) * 16);          // ^ 32 kk
   const int i16 = lane & 15, vr = 4 * half + (i16 >> 2);
   const int vaddr = vr * CP * 16 + (((2 * ((lane >> 4) & 1) + ((i16 >> 1) & 1)) ^ fv<CP>(vr)) * 16) + (i16 & 1) * 8;  // ^ 64 mb
-  float *bias = reinterpret_cast<float *>(lds + G::BIAS) + wave * KT;
+  float *bias = reinterpret_cast<float *>(lds + G::MASKS + wave * G::MASK_WAVE + G::MASK_SLOTS * G::MASK_SLOT);
 
   typedef floatx16 Scores[QB][NKB];
   floatx16 o[QB][MB];
@@ -352,8 +386,9 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   // A slot is one A operand's products and what the vector unit does in their 32
   // cycles each; the fences keep the order, since a wave issues in order and the
   // compiler would put each kind in a run of its own. Operands are read kAhead
-  // slots early.
-  auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top) {
+  // slots early. k_done() follows the last use of the K tile, v_here() precedes
+  // the first read of the V tile.
+  auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top, auto k_done, auto v_here) {
     constexpr int B = decltype(buffer)::value, NEXT = decltype(next)::value;
     constexpr int FIRST = NEXT ? 0 : F_K, SLOTS = F_K + F_V;
     constexpr int kAhead = 3;
@@ -366,6 +401,8 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
     };
     uintx4 p[QB][NKB * 2];
     float sum[QB][2] = {};
+    constexpr bool EARLY = !NEXT || F_K < kAhead;   // the first operands reach into the V tile
+    if constexpr (EARLY) v_here();
     static_for<kAhead>([&](auto i) { fetch(std::integral_constant<int, FIRST + decltype(i)::value>{}); });
     if constexpr (!NEXT) {
       static_for<PAIRS>([&](auto i) {
@@ -377,6 +414,8 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
     }
     static_for<SLOTS - FIRST>([&](auto i) {
       constexpr int U = FIRST + decltype(i)::value;
+      if constexpr (!EARLY && U + kAhead == F_K) v_here();
+      if constexpr (NEXT && U == F_K) k_done();
       fetch(std::integral_constant<int, U + kAhead>{});
       const T8 x = op[U % (kAhead + 1)];
       if constexpr (U < F_K) {
@@ -421,32 +460,72 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   };
 
   // Tile j lies in buffers (j + nt - 1) & 1: the last one in 0.
+  //
+  // Shared tiles: one barrier a step, at its start; behind it every wave has left
+  // the buffers of K tile j and V tile j - 1, which take tiles j + 2 and j + 1.
+  // Own tiles: a buffer is refilled as soon as its wave has read it, so that
+  // three of the four are always on their way (the read of k and v is what such
+  // a call spends its time on): K tile j + 3 between the products of step j, V
+  // tile j + 2 after them. A tile past the last is asked for too, which writes
+  // zeros and keeps the counts.
   if (nt > 0) {
     Scores s0, s1;
     float top[QB];
-    int j = 0, next = mask_byte(2);
-    uint64_t bits1 = __ballot(mask_byte(1) != 0);
-    const uint64_t bits0 = __ballot(mask_byte(0) != 0);
+    int j = 0;
     const int odd = (nt - 1) & 1;
+    uint64_t bits0 = 0, bits1 = 0, bits2 = 0;   // of tiles j, j + 1, j + 2
+    auto none = [] {};
     // Scores of tile j + 1 into n beside the rest of tile j, whose buffers are B.
     auto advance = [&](auto buffer, const Scores &s, Scores &n) {
       constexpr int B = decltype(buffer)::value;
-      arrived();
-      const uint64_t bits2 = __ballot(next != 0);
-      next = mask_byte(j + 3);
-      issue_v(j + 1, 1 - B, bits1);
-      if (j + 2 < nt) issue_k(j + 2, B, bits2);
-      set_bias(bits1);
-      step(buffer, std::integral_constant<int, 1>{}, s, n, top);
+      if constexpr (SHARED) {
+        arrived(std::integral_constant<int, 0>{});
+        bits2 = seen(j + 2);
+        issue_v(j + 1, 1 - B, bits1);
+        if (j + 2 < nt) {
+          issue_mask(j + 3);
+          issue_k(j + 2, B, bits2);
+        }
+        set_bias(bits1);
+        step(buffer, std::integral_constant<int, 1>{}, s, n, top, none, none);
+        bits1 = bits2;
+      } else {
+        uint64_t bits3 = 0;
+        arrived(std::integral_constant<int, 3 * NI + MASK>{});
+        set_bias(bits1);
+        step(buffer, std::integral_constant<int, 1>{}, s, n, top,
+             [&] {
+               bits3 = seen(j + 3);
+               issue_mask(j + 5);
+               issue_k(j + 3, 1 - B, bits3);
+             },
+             [&] { arrived(std::integral_constant<int, 2 * NI + MASK>{}); });
+        issue_v(j + 2, B, bits2);
+        bits1 = bits2;
+        bits2 = bits3;
+      }
       cut(n, j + 1, top);
       follow(top);
-      bits1 = bits2;
       ++j;
     };
+    if constexpr (MASK) {
+#pragma unroll
+      for (int i = 0; i < (SHARED ? 3 : 4); ++i) issue_mask(i);
+      arrived(std::integral_constant<int, 0>{});
+      bits0 = seen(0);
+      bits1 = seen(1);
+      bits2 = seen(2);
+    }
     issue_k(0, odd, bits0);
-    arrived();
-    issue_v(0, odd, bits0);
-    if (nt > 1) issue_k(1, 1 - odd, bits1);
+    if constexpr (SHARED) {
+      arrived(std::integral_constant<int, 0>{});
+      issue_v(0, odd, bits0);
+      if (nt > 1) issue_k(1, 1 - odd, bits1);
+    } else {
+      issue_k(1, 1 - odd, bits1);
+      issue_v(0, odd, bits0);
+      arrived(std::integral_constant<int, 2 * NI>{});
+    }
     set_bias(bits0);
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
@@ -459,6 +538,11 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) s0[qb][kb] = mma(x, qf[qb][kk], s0[qb][kb]);
       }
+    }
+    if constexpr (!SHARED) {
+      issue_mask(4);
+      issue_k(2, odd, bits2);
+      issue_v(1, 1 - odd, bits1);
     }
     maximum(s0, top);
     cut(s0, 0, top);
@@ -474,8 +558,10 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
       advance(std::integral_constant<int, 0>{}, s0, s1);
       advance(std::integral_constant<int, 1>{}, s1, s0);
     }
-    arrived();
-    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, s0, s1, top);
+    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, s0, s1, top, none,
+         [&] { arrived(std::integral_constant<int, SHARED ? 0 : 2 * NI>{}); });
+    // The tiles past the last: LDS is used again below, and by the next workgroup.
+    if constexpr (!SHARED) arrived(std::integral_constant<int, 0>{});
   }
 
   // ---- Results: lane = row n32, elements 32 mb + 8 a + 4 half + (0..3) of o.
@@ -584,12 +670,16 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED>::WAVES)) void is_k11_
   }
 }
 
-// Joins the splits of a row: a thread takes 8 elements.
+// Joins the splits of a row. 2^log_sg neighbouring threads take 8 elements,
+// each the splits of its own, and exchange sums: with few rows, the latency of
+// reading one split after another would be all the time.
 template <typename T>
-__global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int tile_rows, int64_t items) {
+__global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int tile_rows, int log_sg, int64_t items) {
   typedef T T8 __attribute__((ext_vector_type(8)));
-  const int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (it >= items) return;
+  const int64_t thread = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int sg = threadIdx.x & ((1 << log_sg) - 1);
+  const int64_t it = thread >> log_sg;
+  if (it >= items) return;   // whole groups leave
   const int chunks = a.d / 8, e = (int)(it % chunks) * 8;
   const int64_t row = it / chunks;
   const int r = (int)(row % a.rows), bh = (int)(row / a.rows);
@@ -597,18 +687,31 @@ __global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int t
   const int64_t step = (int64_t)a.row_tiles * tile_rows;
   const int64_t at = ((int64_t)bh * a.splits * a.row_tiles + rt) * tile_rows + tr;
   float top = -FLT_MAX, sum = 0.f, f[8] = {};
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, a.part_lse[at + i * step]);
-  for (int i = 0; i < a.splits; ++i) {
-    const float w = __builtin_amdgcn_exp2f(a.part_lse[at + i * step] - top);
+  for (int i = sg; i < a.splits; i += 1 << log_sg) {
+    const float x = a.part_lse[at + i * step];
     const floatx4 *p = reinterpret_cast<const floatx4 *>(a.part + (at + i * step) * a.d + e);
-    const floatx4 x = p[0], y = p[1];
-    sum += w;
+    const floatx4 lo = p[0], hi = p[1];
+    const float next = fmaxf(top, x), old = __builtin_amdgcn_exp2f(top - next), w = __builtin_amdgcn_exp2f(x - next);
+    top = next;
+    sum = sum * old + w;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      f[u] += w * x[u];
-      f[4 + u] += w * y[u];
+      f[u] = f[u] * old + w * lo[u];
+      f[4 + u] = f[4 + u] * old + w * hi[u];
     }
   }
+  float most = top;
+  for (int i = 0; i < log_sg; ++i) most = fmaxf(most, __shfl_xor(most, 1 << i));
+  const float scale = __builtin_amdgcn_exp2f(top - most);
+  sum *= scale;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) f[u] *= scale;
+  for (int i = 0; i < log_sg; ++i) {
+    sum += __shfl_xor(sum, 1 << i);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) f[u] += __shfl_xor(f[u], 1 << i);
+  }
+  if (sg != 0) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   T8 w;
 #pragma unroll
@@ -617,7 +720,7 @@ __global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int t
   *reinterpret_cast<T8 *>(static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2] + e) = w;
   if (a.lse && e == 0)
     a.lse[((int64_t)b * a.hq + h) * a.lq + i] =
-        sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+        sum == 0.f ? -INFINITY : (most + __log2f(sum)) * 0.69314718055994531f;
 }
 
 constexpr int kHeads[] = {32, 64, 96, 128, 160, 192, 256};   // padded head sizes
@@ -653,8 +756,10 @@ hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
   });
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t items = (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8);
-  return launch_kernel(is_k11_attention_join<T>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a,
-                       p.tile_rows, items);
+  int log_sg = 0;
+  while (log_sg < 5 && (1 << log_sg) < p.splits) ++log_sg;
+  return launch_kernel(is_k11_attention_join<T>, dim3((unsigned)(((items << log_sg) + 255) / 256)), dim3(256), 0, s, a,
+                       p.tile_rows, log_sg, items);
 }
 
 }  // namespace
