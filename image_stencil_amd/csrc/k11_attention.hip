@@ -80,22 +80,42 @@ __device__ __forceinline__ floatx16 mma(__bf16 __attribute__((ext_vector_type(8)
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// 16 bytes per lane from a buffer straight into LDS at dst + 16 lane (zeros for
-// an offset outside the buffer). Written as an instruction because the compiler
-// takes the builtin for a store that any later transposing LDS read may meet,
-// and waits for it there; the kernel's own waits (arrived) are what is needed.
-// It has no output register, so nothing is open while it runs. A descriptor that
-// a vector instruction brought to scalar registers needs five wait states before
-// a load may use it: the move and the s_nop.
-__device__ __forceinline__ void dma16(uintx4 rs, unsigned dst, unsigned off) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :
-                   : "s"(dst), "v"(off), "s"(rs)
-                   : "memory");
+// N operations of 16 bytes per lane from a buffer straight into LDS, operation i
+// to dst + i * STEP + 16 lane (zeros for an offset outside the buffer). Written as
+// instructions because the compiler takes the builtin for a store that any later
+// transposing LDS read may meet, and waits for it there; the kernel's own waits
+// (arrived) are what is needed. They have no output register, so nothing is open
+// while they run. The s_nop 4 keeps a descriptor that a vector instruction brought
+// to scalar registers (a spill) five wait states from its first use.
+#define IS_DMA16(O) "buffer_load_dwordx4 " O ", %1, 0 offen lds\n\t"
+#define IS_NEXT "s_add_u32 m0, m0, %c2\n\ts_nop 0\n\t"
+template <int N, int STEP>
+__device__ __forceinline__ void dma16(uintx4 rs, unsigned dst, const unsigned *o) {
+  if constexpr (N >= 4) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\t" IS_DMA16("%3") IS_NEXT IS_DMA16("%4") IS_NEXT IS_DMA16("%5")
+                         IS_NEXT IS_DMA16("%6")
+                     :
+                     : "s"(dst), "s"(rs), "n"(STEP), "v"(o[0]), "v"(o[1]), "v"(o[2]), "v"(o[3])
+                     : "memory", "scc");
+    if constexpr (N > 4) dma16<N - 4, STEP>(rs, dst + 4 * STEP, o + 4);
+  } else if constexpr (N == 2) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\t" IS_DMA16("%3") IS_NEXT IS_DMA16("%4")
+                     :
+                     : "s"(dst), "s"(rs), "n"(STEP), "v"(o[0]), "v"(o[1])
+                     : "memory", "scc");
+  } else {
+    static_assert(N == 1, "a power of two");
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\t" IS_DMA16("%2")
+                     :
+                     : "s"(dst), "s"(rs), "v"(o[0])
+                     : "memory");
+  }
 }
-// The same with 4 bytes per lane.
+#undef IS_DMA16
+#undef IS_NEXT
+// One operation of 4 bytes per lane.
 __device__ __forceinline__ void dma4(uintx4 rs, unsigned dst, unsigned off) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                    :
                    : "s"(dst), "v"(off), "s"(rs)
                    : "memory");
@@ -118,6 +138,16 @@ __device__ __forceinline__ float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The value is computed before this point (the compiler would move sums to where
+// they are used, behind the products they should run beside).
+__device__ __forceinline__ void pin(float &x) { __asm__ volatile("" : "+v"(x)); }
+
+constexpr bool in_time(int f_k, int mb, int operands, int lag, int pairs, int last) {
+  for (int f = 0; f < operands; ++f)
+    if ((f_k + f * mb - 2 * lag) * pairs / last < 4 * (f + 1)) return false;
+  return true;
+}
+
 template <int DP, int NW, bool SHARED, bool MASK>
 struct Geo {
   static constexpr int CP = chunk_pitch(DP);
@@ -126,13 +156,15 @@ struct Geo {
   static constexpr int TILE = KT * CP * 16;                // bytes of a K or V tile
   static constexpr int LOADERS = SHARED ? NW : 1;          // waves that bring a tile
   static constexpr int NI = KT * CP / 64 / LOADERS;        // 1 KB DMA operations of a wave and tile
-  static constexpr int RING = 4 * TILE;                    // K, K, V, V
+  // Buffers of K (as many of V), and steps between the barriers of shared tiles.
+  static constexpr int RB = SHARED && CP <= 8 ? 4 : 2, SP = RB / 2;
+  static constexpr int RING = 2 * RB * TILE;
   static constexpr int JOIN_PITCH = DP + 4;                // floats
   static constexpr int RINGS = SHARED ? RING : NW * RING;
   static constexpr int JOIN = SHARED ? 0 : NW * 32 * (JOIN_PITCH + 2) * 4;
   static constexpr int MASKS = RINGS > JOIN ? RINGS : JOIN;   // a wave's mask bytes, then its bias
   static constexpr int MASK_SLOT = 256, MASK_SLOTS = 4;
-  static constexpr int MASK_WAVE = MASK_SLOTS * MASK_SLOT + KT * 4;
+  static constexpr int MASK_WAVE = MASK_SLOTS * MASK_SLOT + 2 * KT * 4;
   static constexpr int BYTES = MASKS + (MASK ? NW * MASK_WAVE : 0);
   static constexpr int WAVES = BYTES <= 80 * 1024 && NW == 4 ? 2 : 1;   // per SIMD: two workgroups in a CU's LDS
   static_assert(NI >= 1 && NI * 64 * LOADERS == KT * CP, "whole DMA operations");
@@ -145,7 +177,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   typedef float F2 __attribute__((ext_vector_type(2)));
   typedef short S4 __attribute__((ext_vector_type(4)));
   using G = Geo<DP, NW, SHARED, MASK>;
-  constexpr int CP = G::CP, KT = G::KT, NKB = G::NKB, NI = G::NI, KK = DP / 16, MB = DP / 32;
+  constexpr int CP = G::CP, KT = G::KT, NKB = G::NKB, NI = G::NI, KK = DP / 16, MB = DP / 32, RB = G::RB;
   constexpr int ROWS = SHARED ? 32 * QB * NW : 32;
   __shared__ __attribute__((aligned(1024))) char lds[G::BYTES];
   lds_poison(lds, sizeof(lds));
@@ -202,11 +234,24 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     const uintx4 rs = descriptor((uint64_t)(uintptr_t)base + (uint64_t)((int64_t)key * tok),
                                  left > 0 ? (unsigned)((left - 1) * tok + a.d * 2) : 0u);
     auto all = [&](auto whole) {
+      unsigned o[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const bool see = decltype(whole)::value || (MASK ? (bits >> drow[i]) & 1 : drow[i] < left);
-        dma16(rs, dst + (unsigned)(i * G::LOADERS + (SHARED ? wave : 0)) * 1024u, see ? off[i] : kOob);
+        if constexpr (decltype(whole)::value) {
+          o[i] = off[i];
+        } else if constexpr (MASK) {
+          // All ones where the row's bit is set: one bit-field extract and one select.
+          constexpr int SPAN = G::LOADERS * 64 / CP;   // rows of an operation
+          const int r = drow[i];
+          const bool low = KT == 32 || (SPAN <= 32 ? i * SPAN < 32 : r < 32);
+          const int word = low ? (int)bits : (int)(bits >> 32);
+          const unsigned m = (unsigned)__builtin_amdgcn_sbfe(word, (unsigned)(r & 31), 1);
+          o[i] = (off[i] & m) | (kOob & ~m);
+        } else {
+          o[i] = drow[i] < left ? off[i] : kOob;
+        }
       }
+      dma16<NI, G::LOADERS * 1024>(rs, dst + (SHARED ? wave : 0) * 1024u, o);
     };
     if (MASK ? !~(bits | (KT == 64 ? 0 : ~(uint64_t)0 << (KT & 63))) : left == KT) all(std::true_type{});
     else all(std::false_type{});
@@ -215,7 +260,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     issue(kbase, ktok, koff, tile_key(j), ring_at + buffer * G::TILE, bits);
   };
   auto issue_v = [&](int j, int buffer, uint64_t bits) {
-    issue(vbase, vtok, voff, tile_key(j), ring_at + (2 + buffer) * G::TILE, bits);
+    issue(vbase, vtok, voff, tile_key(j), ring_at + (RB + buffer) * G::TILE, bits);
   };
   // At most N of this wave's DMA operations still out, then (a shared tile)
   // every wave's.
@@ -293,29 +338,29 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   };
   auto v_operand = [&](int buffer, int f) -> T8 {
     typedef __attribute__((address_space(3))) S4 *P;
-    const char *p = ring + (2 + buffer) * G::TILE + (f / MB) * 16 * CP * 16 + (vaddr ^ (f % MB * 64));
+    const char *p = ring + (RB + buffer) * G::TILE + (f / MB) * 16 * CP * 16 + (vaddr ^ (f % MB * 64));
     const S4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
     const S4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 8 * CP * 16));
     return __builtin_bit_cast(T8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   // What the scores of 32 keys start from.
-  auto start = [&](int kb) -> floatx16 {
+  auto start = [&](int slot, int kb) -> floatx16 {
     floatx16 init;
 #pragma unroll
     for (int e = 0; e < 16; ++e) init[e] = 0.f;
     if constexpr (MASK) {
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
-        const floatx4 f = *reinterpret_cast<const floatx4 *>(bias + kb * 32 + 2 * e + 4 * half);
+        const floatx4 f = *reinterpret_cast<const floatx4 *>(bias + slot * KT + kb * 32 + 2 * e + 4 * half);
 #pragma unroll
         for (int u = 0; u < 4; ++u) init[e + u] = f[u];
       }
     }
     return init;
   };
-  auto set_bias = [&](uint64_t bits) {
+  auto set_bias = [&](int slot, uint64_t bits) {   // of a tile: slot tile % 2
     if constexpr (MASK) {
-      if (lane < KT) bias[lane] = (bits >> lane) & 1 ? 0.f : -INFINITY;
+      if (lane < KT) bias[slot * KT + lane] = (bits >> lane) & 1 ? 0.f : -INFINITY;
     }
   };
   // The largest score of every row, in M's unit; half of the lanes' maximum
@@ -371,47 +416,71 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
         for (int e = 0; e < 16; ++e) o[qb][mb][e] *= f;
     }
   };
-  // Two exponentials: p, rounded to T for the second product (the matrix cores
-  // take no wider operand); the sum l takes them in 32 bits.
-  auto exponentials = [&](float s0, float s1, int qb, float &sum) -> unsigned {
-    const F2 p = {__builtin_amdgcn_exp2f(__builtin_fmaf(s0, a.c, -m[qb])),
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(s1, a.c, -m[qb]))};
+  // Two exponentials in three parts, which run in slots of their own so that none
+  // waits for the one before it: the exponents, their powers, and p: rounded to T
+  // for the second product (the matrix cores take no wider operand), while the sum
+  // l takes it in 32 bits.
+  auto exponents = [&](float s0, float s1, int qb) -> F2 {
+    return F2{__builtin_fmaf(s0, a.c, -m[qb]), __builtin_fmaf(s1, a.c, -m[qb])};
+  };
+  auto powers = [&](F2 x) -> F2 { return F2{__builtin_amdgcn_exp2f(x[0]), __builtin_amdgcn_exp2f(x[1])}; };
+  auto weights = [&](F2 p, float &sum) -> unsigned {
     sum += p[0];
     sum += p[1];
     return __builtin_bit_cast(unsigned, __builtin_convertvector(p, T2));
   };
 
-  // One step: scores of the next tile (NEXT: into n, from K buffer 1 - B) beside
-  // the exponentials of s, then s's p v (V buffer B) beside the next maximum.
+  // One step: scores of the next tile (NEXT: into n, from the K buffer after B)
+  // beside the exponentials of s, then s's p v (V buffer B) beside the next maximum.
   // A slot is one A operand's products and what the vector unit does in their 32
   // cycles each; the fences keep the order, since a wave issues in order and the
   // compiler would put each kind in a run of its own. Operands are read kAhead
   // slots early. k_done() follows the last use of the K tile, v_here() precedes
   // the first read of the V tile.
   auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top, auto k_done, auto v_here) {
-    constexpr int B = decltype(buffer)::value, NEXT = decltype(next)::value;
+    const int B = buffer;   // a constant where the loop is unrolled
+    constexpr int NEXT = decltype(next)::value;
     constexpr int FIRST = NEXT ? 0 : F_K, SLOTS = F_K + F_V;
     constexpr int kAhead = 3;
-    constexpr int PAIRS = NKB * 8, LAST = F_K + F_V - MB;   // the last p must be there at slot LAST
+    // Pairs of p: part one of pair i in slot i LAST / PAIRS, the others LAG slots
+    // later each; the last four must be there at slot F_K + F_V - MB.
+    constexpr int PAIRS = NKB * 8, LAG = F_K < 4 ? 0 : 1, LAST = F_K + F_V - MB - 2 * LAG;
+    static_assert(in_time(F_K, MB, NKB * 2, LAG, PAIRS, LAST), "an operand of P is whole before its first product");
     T8 op[kAhead + 1];
     auto fetch = [&](auto f) {
       constexpr int F = decltype(f)::value;
-      if constexpr (F < F_K) op[F % (kAhead + 1)] = k_operand(1 - B, F);
+      if constexpr (F < F_K) op[F % (kAhead + 1)] = k_operand((B + 1) % RB, F);
       else if constexpr (F < SLOTS) op[F % (kAhead + 1)] = v_operand(B, F - F_K);
     };
+    F2 x[QB][PAIRS];
     uintx4 p[QB][NKB * 2];
     float sum[QB][2] = {};
-    constexpr bool EARLY = !NEXT || F_K < kAhead;   // the first operands reach into the V tile
-    if constexpr (EARLY) v_here();
-    static_for<kAhead>([&](auto i) { fetch(std::integral_constant<int, FIRST + decltype(i)::value>{}); });
-    if constexpr (!NEXT) {
-      static_for<PAIRS>([&](auto i) {
-        constexpr int P = decltype(i)::value;
+    // Parts of the pairs [from, to).
+    auto part = [&](auto which, auto from, auto to) {
+      constexpr int W = decltype(which)::value, P0 = decltype(from)::value, P1 = decltype(to)::value;
+      static_for<(P1 > P0 ? P1 - P0 : 0)>([&](auto k) {
+        constexpr int P = P0 + decltype(k)::value;
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb)
-          p[qb][P / 4][P % 4] = exponentials(s[qb][P / 8][2 * (P % 8)], s[qb][P / 8][2 * (P % 8) + 1], qb, sum[qb][P & 1]);
+        for (int qb = 0; qb < QB; ++qb) {
+          if constexpr (W == 0) x[qb][P] = exponents(s[qb][P / 8][2 * (P % 8)], s[qb][P / 8][2 * (P % 8) + 1], qb);
+          if constexpr (W == 1) x[qb][P] = powers(x[qb][P]);
+          if constexpr (W == 2) p[qb][P / 4][P % 4] = weights(x[qb][P], sum[qb][P & 1]);
+        }
       });
-    }
+    };
+    constexpr bool EARLY = !NEXT || F_K < kAhead;   // the first operands reach into the V tile
+    // What the scores start from is read as early as the operands.
+    auto begin = [&](auto block) {
+      constexpr int kb = decltype(block)::value;
+      const floatx16 init = start((B + 1) % 2, kb);
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) n[qb][kb] = init;
+    };
+    if constexpr (EARLY) v_here();
+    if constexpr (NEXT) begin(std::integral_constant<int, 0>{});
+    static_for<kAhead>([&](auto i) { fetch(std::integral_constant<int, FIRST + decltype(i)::value>{}); });
+    if constexpr (!NEXT)
+      static_for<3>([&](auto w) { part(w, std::integral_constant<int, 0>{}, std::integral_constant<int, PAIRS>{}); });
     static_for<SLOTS - FIRST>([&](auto i) {
       constexpr int U = FIRST + decltype(i)::value;
       if constexpr (!EARLY && U + kAhead == F_K) v_here();
@@ -420,11 +489,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
       const T8 x = op[U % (kAhead + 1)];
       if constexpr (U < F_K) {
         constexpr int kb = U / KK, kk = U % KK;
-        if constexpr (kk == 0) {
-          const floatx16 init = start(kb);
-#pragma unroll
-          for (int qb = 0; qb < QB; ++qb) n[qb][kb] = init;
-        }
+        if constexpr (kk == KK - 2 && kb + 1 < NKB) begin(std::integral_constant<int, kb + 1>{});
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) n[qb][kb] = mma(x, qf[qb][kk], n[qb][kb]);
       } else {
@@ -433,14 +498,13 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
         for (int qb = 0; qb < QB; ++qb) o[qb][mb] = mma(x, __builtin_bit_cast(T8, p[qb][f]), o[qb][mb]);
       }
       if constexpr (NEXT) {
-        // Pairs of exponentials: evenly over the slots before LAST.
-        constexpr int P0 = U < LAST ? U * PAIRS / LAST : PAIRS, P1 = U < LAST ? (U + 1) * PAIRS / LAST : PAIRS;
-        static_for<P1 - P0>([&](auto k) {
-          constexpr int P = P0 + decltype(k)::value;
-#pragma unroll
-          for (int qb = 0; qb < QB; ++qb)
-            p[qb][P / 4][P % 4] =
-                exponentials(s[qb][P / 8][2 * (P % 8)], s[qb][P / 8][2 * (P % 8) + 1], qb, sum[qb][P & 1]);
+        static_for<3>([&](auto w) {   // the oldest first
+          constexpr int W = 2 - decltype(w)::value, V = U - W * LAG;
+          constexpr int P0 = V < 0 ? 0 : V < LAST ? V * PAIRS / LAST : PAIRS;
+          constexpr int P1 = V < 0 ? 0 : V < LAST ? (V + 1) * PAIRS / LAST : PAIRS;
+          // With LAG 0 the parts of one slot run in their own order.
+          constexpr int R = LAG ? W : 2 - W;
+          part(std::integral_constant<int, R>{}, std::integral_constant<int, P0>{}, std::integral_constant<int, P1>{});
         });
         // The next scores' maximum: evenly over the V slots but the first.
         if constexpr (U > F_K) {
@@ -450,7 +514,13 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
             if constexpr (E0 == 0) top[qb] = n[qb][0][0];
 #pragma unroll
             for (int e = E0; e < E1; ++e) top[qb] = fmaxf(top[qb], n[qb][e / 16][e % 16]);
+            pin(top[qb]);
           }
+        }
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+          pin(sum[qb][0]);
+          pin(sum[qb][1]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -459,10 +529,12 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     for (int qb = 0; qb < QB; ++qb) l[qb] += sum[qb][0] + sum[qb][1];
   };
 
-  // Tile j lies in buffers (j + nt - 1) & 1: the last one in 0.
+  // Tile j lies in buffers j % RB.
   //
-  // Shared tiles: one barrier a step, at its start; behind it every wave has left
-  // the buffers of K tile j and V tile j - 1, which take tiles j + 2 and j + 1.
+  // Shared tiles: a barrier every SP steps (two where LDS has room, since a
+  // barrier is a wait for the slowest of four waves); behind that of step j every
+  // wave has left K tile j, V tile j - 1 and those before, and their buffers take
+  // the next SP tiles.
   // Own tiles: a buffer is refilled as soon as its wave has read it, so that
   // three of the four are always on their way (the read of k and v is what such
   // a call spends its time on): K tile j + 3 between the products of step j, V
@@ -471,94 +543,105 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   if (nt > 0) {
     Scores s0, s1;
     float top[QB];
+    constexpr int SP = G::SP;
     int j = 0;
-    const int odd = (nt - 1) & 1;
-    uint64_t bits0 = 0, bits1 = 0, bits2 = 0;   // of tiles j, j + 1, j + 2
+    uint64_t bits[SP + 1] = {};   // of tiles j + SP .. j + 2 SP; own tiles: bits[0] of j + 2
     auto none = [] {};
-    // Scores of tile j + 1 into n beside the rest of tile j, whose buffers are B.
-    auto advance = [&](auto buffer, const Scores &s, Scores &n) {
-      constexpr int B = decltype(buffer)::value;
+    // Scores of tile j + 1 into n beside the rest of tile j; u = j % RB.
+    auto advance = [&](auto u, const Scores &s, Scores &n) {
+      constexpr int B = decltype(u)::value;
       if constexpr (SHARED) {
-        arrived(std::integral_constant<int, 0>{});
-        bits2 = seen(j + 2);
-        issue_v(j + 1, 1 - B, bits1);
-        if (j + 2 < nt) {
-          issue_mask(j + 3);
-          issue_k(j + 2, B, bits2);
+        if constexpr (B % SP == 0) {
+          arrived(std::integral_constant<int, 0>{});
+#pragma unroll
+          for (int i = 0; i <= SP; ++i) bits[i] = seen(j + SP + i);
+#pragma unroll
+          for (int i = 1; i <= SP; ++i) issue_mask(j + 2 * SP + i);
+#pragma unroll
+          for (int i = 0; i < SP; ++i)
+            if (j > 0) issue_v(j + SP + i, (B + SP + i) % RB, bits[i]);
+#pragma unroll
+          for (int i = 1; i <= SP; ++i)
+            if (j > 0 || i == SP) issue_k(j + SP + i, (B + SP + i) % RB, bits[i]);
         }
-        set_bias(bits1);
-        step(buffer, std::integral_constant<int, 1>{}, s, n, top, none, none);
-        bits1 = bits2;
+        set_bias(B % 2, bits[SP == 1 ? 1 : B % SP]);   // of tile j + 2
+        step(u, std::integral_constant<int, 1>{}, s, n, top, none, none);
       } else {
-        uint64_t bits3 = 0;
+        uint64_t next = 0;
         arrived(std::integral_constant<int, 3 * NI + MASK>{});
-        set_bias(bits1);
-        step(buffer, std::integral_constant<int, 1>{}, s, n, top,
+        step(u, std::integral_constant<int, 1>{}, s, n, top,
              [&] {
-               bits3 = seen(j + 3);
+               next = seen(j + 3);
+               set_bias((B + 1) % 2, next);
                issue_mask(j + 5);
-               issue_k(j + 3, 1 - B, bits3);
+               issue_k(j + 3, (B + 3) % RB, next);
              },
              [&] { arrived(std::integral_constant<int, 2 * NI + MASK>{}); });
-        issue_v(j + 2, B, bits2);
-        bits1 = bits2;
-        bits2 = bits3;
+        issue_v(j + 2, B, bits[0]);
+        bits[0] = next;
       }
       cut(n, j + 1, top);
       follow(top);
       ++j;
     };
+    // The first tiles: every buffer is asked for at once, so that a short row of
+    // keys costs one trip to memory.
+    uint64_t early[RB] = {};
     if constexpr (MASK) {
 #pragma unroll
-      for (int i = 0; i < (SHARED ? 3 : 4); ++i) issue_mask(i);
+      for (int i = 0; i < (SHARED ? RB : 4); ++i) issue_mask(i);
       arrived(std::integral_constant<int, 0>{});
-      bits0 = seen(0);
-      bits1 = seen(1);
-      bits2 = seen(2);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) early[i] = seen(i);
+      if constexpr (SHARED) issue_mask(RB);
+      else bits[0] = seen(2);
     }
-    issue_k(0, odd, bits0);
-    if constexpr (SHARED) {
-      arrived(std::integral_constant<int, 0>{});
-      issue_v(0, odd, bits0);
-      if (nt > 1) issue_k(1, 1 - odd, bits1);
-    } else {
-      issue_k(1, 1 - odd, bits1);
-      issue_v(0, odd, bits0);
-      arrived(std::integral_constant<int, 2 * NI>{});
-    }
-    set_bias(bits0);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) issue_k(i, i, early[i]);
+#pragma unroll
+    for (int i = 0; i < (SHARED ? RB : 1); ++i) issue_v(i, i, early[i]);
+    arrived(std::integral_constant<int, (RB - 1 + (SHARED ? RB : 1)) * NI>{});
+    set_bias(0, early[0]);
+    set_bias(1, early[1]);
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
-      const floatx16 init = start(kb);
+      const floatx16 init = start(0, kb);
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb) s0[qb][kb] = init;
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        const T8 x = k_operand(odd, kb * KK + kk);
+        const T8 x = k_operand(0, kb * KK + kk);
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) s0[qb][kb] = mma(x, qf[qb][kk], s0[qb][kb]);
       }
     }
     if constexpr (!SHARED) {
+      set_bias(0, bits[0]);
       issue_mask(4);
-      issue_k(2, odd, bits2);
-      issue_v(1, 1 - odd, bits1);
+      issue_k(2, 0, bits[0]);
+      issue_v(1, 1, early[1]);
     }
     maximum(s0, top);
     cut(s0, 0, top);
     follow(top);
-    if (odd) {
+    bool more = nt > 1;
+    while (more) {
+      static_for<RB>([&](auto u) {
+        if (!more) return;
+        if constexpr (decltype(u)::value % 2 == 0) advance(u, s0, s1);
+        else advance(u, s1, s0);
+        more = j + 1 < nt;
+        if constexpr (decltype(u)::value % 2 == 0) {
+          if (!more) {
 #pragma unroll
-      for (int qb = 0; qb < QB; ++qb)
+            for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) s1[qb][kb] = s0[qb][kb];
-      advance(std::integral_constant<int, 1>{}, s1, s0);
+              for (int kb = 0; kb < NKB; ++kb) s0[qb][kb] = s1[qb][kb];
+          }
+        }
+      });
     }
-    while (j + 1 < nt) {
-      advance(std::integral_constant<int, 0>{}, s0, s1);
-      advance(std::integral_constant<int, 1>{}, s1, s0);
-    }
-    step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, s0, s1, top, none,
+    step(j % RB, std::integral_constant<int, 0>{}, s0, s1, top, none,
          [&] { arrived(std::integral_constant<int, SHARED ? 0 : 2 * NI>{}); });
     // The tiles past the last: LDS is used again below, and by the next workgroup.
     if constexpr (!SHARED) arrived(std::integral_constant<int, 0>{});
