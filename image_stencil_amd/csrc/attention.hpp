@@ -47,6 +47,7 @@ struct AttentionPlan {
   int row_tiles;
   int splits;             // workgroups the keys of one row tile are split over
   int split_keys;         // keys per split, a multiple of the key tile
+  int run;                // row tiles a workgroup goes through
   int block, lds;
   int64_t units;          // n * hkv * row_tiles
 };

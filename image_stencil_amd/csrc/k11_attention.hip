@@ -42,6 +42,21 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
 
+// n / d for 0 <= n < 2^31 by a product: with 2^(s - 1) < d <= 2^s and
+// m = ceil(2^(31 + s) / d), n m >> 31 + s is exact. (The index arithmetic of a
+// workgroup would otherwise spend four divisions before its first load.)
+struct Divisor {
+  unsigned m, s;
+};
+Divisor divisor(unsigned d) {
+  unsigned s = 0;
+  while (((uint64_t)1 << s) < d) ++s;
+  return {(unsigned)((((uint64_t)1 << (31 + s)) + d - 1) / d), s};
+}
+__device__ __forceinline__ int divide(int n, Divisor d) {
+  return (int)(((uint64_t)(unsigned)n * d.m) >> (31 + d.s));
+}
+
 struct Args {
   const void *q, *k, *v;
   const uint8_t *mask;
@@ -51,7 +66,9 @@ struct Args {
   float *part;            // splits > 1: O / l of every block, [block][tile row][d]
   float *part_lse;        // and M + log2 l, [block][tile row]
   int64_t qs[3], ks[3], vs[3], os[3], mask_bs;
-  int lq, lk, hq, hkv, d, group, rows, row_tiles, splits, split_keys, groups;
+  int lq, lk, hq, hkv, d, group, rows, row_tiles, splits, split_keys, groups, runs;
+  int run;                // row tiles a workgroup goes through
+  Divisor by_group, by_runs, by_splits, by_hkv;
   unsigned flip;          // sign bits of a negative scale
   float c;                // |scale| log2(e)
 };
@@ -170,7 +187,9 @@ struct Geo {
   static_assert(NI >= 1 && NI * 64 * LOADERS == KT * CP, "whole DMA operations");
 };
 
-template <typename T, int DP, int QB, int NW, bool SHARED, bool MASK>
+// RESIDENT (with SHARED): all keys fit the buffers, and a workgroup goes through
+// a.run row tiles with them, the next one's queries on their way.
+template <typename T, int DP, int QB, int NW, bool SHARED, bool RESIDENT, bool MASK>
 __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void is_k11_attention(const Args a) {
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef T T2 __attribute__((ext_vector_type(2)));
@@ -188,19 +207,13 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   // Workgroup -> (entry and key head, split, row tile). Row tiles of a group
   // read the same keys, so a group stays on one XCD: groups are dealt to the 8
   // XCDs in turn, or in one run of consecutive tiles where 8 does not divide them.
-  int g, rt;
-  if ((a.groups & 7) == 0) {
-    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
-    g = (i / a.row_tiles) * 8 + x;
-    rt = i % a.row_tiles;
-  } else {
-    const int i = xcd_remap(blockIdx.x, gridDim.x);
-    g = i / a.row_tiles;
-    rt = i % a.row_tiles;
-  }
-  const int split = g % a.splits, bh = g / a.splits;
-  const int hk = bh % a.hkv, b = bh / a.hkv;
-  const int row0 = rt * ROWS + (SHARED ? wave * 32 * QB : 0);
+  const bool dealt = (a.groups & 7) == 0;
+  const int place = dealt ? (int)(blockIdx.x >> 3) : xcd_remap(blockIdx.x, gridDim.x);
+  const int turn = divide(place, a.by_runs);
+  const int g = dealt ? turn * 8 + (int)(blockIdx.x & 7) : turn;
+  const int rt0 = (place - turn * a.runs) * (RESIDENT ? a.run : 1);
+  const int bh = divide(g, a.by_splits), split = g - bh * a.splits;
+  const int b = divide(bh, a.by_hkv), hk = bh - b * a.hkv;
 
   int len = a.lk;
   if (a.lengths) len = min(len, max(0, a.lengths[b]));
@@ -295,21 +308,28 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
 
   // ---- Queries: B operands, lane = row n32, elements 16 kk + 8 half .. + 7.
   T8 qf[QB][KK];
+  uintx4 qw[QB][KK];   // of the row tile after, on their way
+  auto load_q = [&](int rt) {
 #pragma unroll
-  for (int qb = 0; qb < QB; ++qb) {
-    const int r = row0 + qb * 32 + n32;
-    const int i = r / a.group, h = hk * a.group + r % a.group;
-    const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2];
+    for (int qb = 0; qb < QB; ++qb) {
+      const int r = rt * ROWS + (SHARED ? wave * 32 * QB : 0) + qb * 32 + n32;
+      const int i = divide(r, a.by_group), h = hk * a.group + r - i * a.group;
+      const T *p = static_cast<const T *>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2];
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      uintx4 w = {0, 0, 0, 0};
-      if (r < a.rows && (2 * kk + half) * 8 < a.d) {
-        w = *reinterpret_cast<const uintx4 *>(p + (2 * kk + half) * 8);
-        w ^= a.flip;
+      for (int kk = 0; kk < KK; ++kk) {
+        qw[qb][kk] = uintx4{0, 0, 0, 0};
+        if (r < a.rows && (2 * kk + half) * 8 < a.d)
+          qw[qb][kk] = *reinterpret_cast<const uintx4 *>(p + (2 * kk + half) * 8);
       }
-      qf[qb][kk] = __builtin_bit_cast(T8, w);
     }
-  }
+  };
+  auto take_q = [&]() {
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) qf[qb][kk] = __builtin_bit_cast(T8, qw[qb][kk] ^ a.flip);
+  };
+  load_q(rt0);
 
   // ---- LDS read addresses (bytes in a tile).
   const int kaddr = n32 * CP * 16 + ((half ^ fk<CP>(n32)) * 16);          // ^ 32 kk
@@ -320,15 +340,6 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   typedef floatx16 Scores[QB][NKB];
   floatx16 o[QB][MB];
   float m[QB], l[QB];
-#pragma unroll
-  for (int qb = 0; qb < QB; ++qb) {
-    m[qb] = -FLT_MAX;
-    l[qb] = 0.f;
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[qb][mb][e] = 0.f;
-  }
 
   // A operands in the order of their use: F_K of a K tile, F_V of a V tile.
   constexpr int F_K = NKB * KK, F_V = NKB * 2 * MB;
@@ -381,7 +392,8 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     if constexpr (!MASK) {
       const int left = keys - tile_key(j);
       if (left >= KT) return;
-      const int mine = left - 4 * half;
+      int mine = left - 4 * half;
+      __asm__ volatile("" : "+v"(mine));   // kept from leaving a loop over row tiles as 32 masks
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
@@ -540,6 +552,17 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   // a call spends its time on): K tile j + 3 between the products of step j, V
   // tile j + 2 after them. A tile past the last is asked for too, which writes
   // zeros and keeps the counts.
+  uint64_t early[RB] = {};   // of the first tiles
+  auto row_tile = [&](const int rt, const bool again, const bool another) {
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    m[qb] = -FLT_MAX;
+    l[qb] = 0.f;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[qb][mb][e] = 0.f;
+  }
   if (nt > 0) {
     Scores s0, s1;
     float top[QB];
@@ -551,7 +574,11 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     auto advance = [&](auto u, const Scores &s, Scores &n) {
       constexpr int B = decltype(u)::value;
       if constexpr (SHARED) {
-        if constexpr (B % SP == 0) {
+        if constexpr (RESIDENT) {
+          // All tiles came with the first row tile's.
+          if (B == 0 && !again) arrived(std::integral_constant<int, 0>{});
+          bits[SP == 1 ? 1 : B % SP] = B + 2 < RB ? early[B + 2] : 0;
+        } else if constexpr (B % SP == 0) {
           arrived(std::integral_constant<int, 0>{});
 #pragma unroll
           for (int i = 0; i <= SP; ++i) bits[i] = seen(j + SP + i);
@@ -586,21 +613,24 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     };
     // The first tiles: every buffer is asked for at once, so that a short row of
     // keys costs one trip to memory.
-    uint64_t early[RB] = {};
+    if (!again) {
     if constexpr (MASK) {
 #pragma unroll
       for (int i = 0; i < (SHARED ? RB : 4); ++i) issue_mask(i);
       arrived(std::integral_constant<int, 0>{});
 #pragma unroll
       for (int i = 0; i < RB; ++i) early[i] = seen(i);
-      if constexpr (SHARED) issue_mask(RB);
-      else bits[0] = seen(2);
+      if constexpr (!SHARED) bits[0] = seen(2);
+      else if constexpr (!RESIDENT) issue_mask(RB);
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i) issue_k(i, i, early[i]);
 #pragma unroll
     for (int i = 0; i < (SHARED ? RB : 1); ++i) issue_v(i, i, early[i]);
     arrived(std::integral_constant<int, (RB - 1 + (SHARED ? RB : 1)) * NI>{});
+    }
+    take_q();
+    if (another) load_q(rt + 1);
     set_bias(0, early[0]);
     set_bias(1, early[1]);
 #pragma unroll
@@ -642,7 +672,9 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
       });
     }
     step(j % RB, std::integral_constant<int, 0>{}, s0, s1, top, none,
-         [&] { arrived(std::integral_constant<int, SHARED ? 0 : 2 * NI>{}); });
+         [&] {
+           if (!again) arrived(std::integral_constant<int, SHARED ? 0 : 2 * NI>{});
+         });
     // The tiles past the last: LDS is used again below, and by the next workgroup.
     if constexpr (!SHARED) arrived(std::integral_constant<int, 0>{});
   }
@@ -673,7 +705,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
           if (half == 0) a.part_lse[at] = l[qb] == 0.f ? -INFINITY : m[qb] + __log2f(l[qb]);
         }
       } else {
-        const int i = r / a.group, h = hk * a.group + r % a.group;
+        const int i = divide(r, a.by_group), h = hk * a.group + r - i * a.group;
         T *p = static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
@@ -742,7 +774,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
         p[1] = floatx4{f[4], f[5], f[6], f[7]};
         if (e == 0) a.part_lse[at] = lse2;
       } else {
-        const int i = r / a.group, h = hk * a.group + r % a.group;
+        const int i = divide(r, a.by_group), h = hk * a.group + r - i * a.group;
         T8 w;
 #pragma unroll
         for (int y = 0; y < 8; ++y) w[y] = (T)f[y];
@@ -750,6 +782,13 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
         if (a.lse && e == 0) a.lse[((int64_t)b * a.hq + h) * a.lq + i] = lse2 * 0.69314718055994531f;
       }
     }
+  }
+  };
+  if constexpr (RESIDENT) {
+    const int rt1 = min(rt0 + a.run, a.row_tiles);
+    for (int rt = rt0; rt < rt1; ++rt) row_tile(rt, rt > rt0, rt + 1 < rt1);
+  } else {
+    row_tile(rt0, false, false);
   }
 }
 
@@ -822,20 +861,25 @@ hipError_t for_head(int dp, F &&f) {
   }
 }
 
+constexpr int kResidentHead = 128;   // the largest padded head with a RESIDENT form
 constexpr int few_waves(int dp) { return dp <= 128 ? 4 : 2; }
 
 template <typename T>
 hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
-  const unsigned blocks = (unsigned)(p.units * p.splits);
+  const unsigned blocks = (unsigned)((int64_t)a.groups * a.runs);
   hipError_t e = for_head(p.dp, [&](auto dp) -> hipError_t {
     constexpr int DP = decltype(dp)::value;
-    if (p.tile_rows == 32) {
-      constexpr int NW = few_waves(DP);
-      return a.mask ? launch_kernel(is_k11_attention<T, DP, 1, NW, false, true>, dim3(blocks), dim3(NW * 64), 0, s, a)
-                    : launch_kernel(is_k11_attention<T, DP, 1, NW, false, false>, dim3(blocks), dim3(NW * 64), 0, s, a);
-    }
-    return a.mask ? launch_kernel(is_k11_attention<T, DP, 1, 4, true, true>, dim3(blocks), dim3(256), 0, s, a)
-                  : launch_kernel(is_k11_attention<T, DP, 1, 4, true, false>, dim3(blocks), dim3(256), 0, s, a);
+    auto go = [&](auto waves, auto shared, auto resident) -> hipError_t {
+      constexpr int NW = decltype(waves)::value;
+      constexpr bool S = decltype(shared)::value, R = decltype(resident)::value;
+      return a.mask ? launch_kernel(is_k11_attention<T, DP, 1, NW, S, R, true>, dim3(blocks), dim3(NW * 64), 0, s, a)
+                    : launch_kernel(is_k11_attention<T, DP, 1, NW, S, R, false>, dim3(blocks), dim3(NW * 64), 0, s, a);
+    };
+    using four = std::integral_constant<int, 4>;
+    if (p.tile_rows == 32) return go(std::integral_constant<int, few_waves(DP)>{}, std::false_type{}, std::false_type{});
+    if constexpr (DP <= kResidentHead)
+      if (p.run > 1) return go(four{}, std::true_type{}, std::true_type{});
+    return go(four{}, std::true_type{}, std::false_type{});
   });
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t items = (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8);
@@ -870,6 +914,15 @@ bool configure_attention(AttentionPlan &p) {
   if (p.split_keys < tile) p.split_keys = tile;
   p.splits = (int)((d.lk + (int64_t)p.split_keys - 1) / p.split_keys);
   if (p.splits < 1) p.splits = 1;
+  // Few keys and many row tiles: a workgroup keeps the keys for several, which
+  // leaves one round of workgroups. (One tile each: the trip to memory, the
+  // products and the stores of one row tile follow each other in every workgroup.)
+  const int kept = p.dp <= 64 ? 4 : 2;   // tiles that fit the buffers
+  p.run = 1;
+  if (!few && p.splits == 1 && p.dp <= kResidentHead && d.lk <= kept * 64) {
+    const int64_t run = p.units / slots;
+    p.run = (int)(run < 1 ? 1 : run > p.row_tiles ? p.row_tiles : run);
+  }
   return p.units * p.splits <= 2147483647;
 }
 
@@ -909,6 +962,12 @@ hipError_t launch_attention(const AttentionPlan &p, const void *q, const void *k
   a.splits = p.splits;
   a.split_keys = p.split_keys;
   a.groups = d.n * d.hkv * p.splits;
+  a.run = p.run;
+  a.runs = (p.row_tiles + p.run - 1) / p.run;
+  a.by_group = divisor((unsigned)p.group);
+  a.by_runs = divisor((unsigned)a.runs);
+  a.by_splits = divisor((unsigned)p.splits);
+  a.by_hkv = divisor((unsigned)d.hkv);
   a.flip = p.scale < 0.f ? 0x80008000u : 0u;
   a.c = (float)(fabs((double)p.scale) * 1.4426950408889634);
   return d.dtype == IS_F16 ? launch_t<_Float16>(p, a, s) : launch_t<__bf16>(p, a, s);
