@@ -109,7 +109,7 @@ void frequencies(is::RotaryPlan &p) {
       f = f * keep + f / d.factor * (1.0 - keep);
     }
     p.freq[i] = f;
-    p.turns[i] = f / kTwoPi;
+    for (int axis = 0; axis < d.axes; ++axis) p.turns[axis * per + i] = f / kTwoPi;
   }
 }
 
@@ -151,9 +151,9 @@ is_status run_rotary(const is::RotaryPlan &p, is_dtype dtype, int norm, float ep
     const is_status st = check_part(p, dtype, parts[i]);
     if (st != IS_OK) return st;
   }
-  const int vec = is::rotary_vector_width(p, dtype, parts, nparts);
+  const int vec = is::rotary_vector_width(p, dtype);
   double blocks = 0.0;
-  for (int i = 0; i < nparts; ++i) blocks += (double)is::rotary_blocks(p, dtype, vec, parts[i].xt);
+  for (int i = 0; i < nparts; ++i) blocks += (double)is::rotary_blocks(p, vec, parts[i].xt);
   if (blocks > 2147483647.0) return IS_ERR_UNSUPPORTED;
   if (blocks == 0.0) return IS_OK;
   return is::report_hip(is::launch_rotary(p, dtype, norm, eps, parts, nparts, stream));

@@ -14,7 +14,7 @@ struct RotaryPlan {
   rotary_desc d;
   int per_axis;                          // Pa = rot / 2 / axes
   double freq[IS_MAX_HEAD_DIM / 2];      // radians per position
-  double turns[IS_MAX_HEAD_DIM / 2];     // turns per position
+  double turns[IS_MAX_HEAD_DIM / 2];     // turns per position, of every pair (axis after axis)
 };
 
 // One tensor of a rotary launch.
@@ -30,11 +30,11 @@ struct RotaryPart {
 // norm: 0 (none), IS_NORM_RMS or IS_NORM_LAYER. parts with no element are skipped.
 hipError_t launch_rotary(const RotaryPlan &p, is_dtype dtype, int norm, float eps, const RotaryPart *parts,
                          int nparts, hipStream_t s);
-// Elements a lane of the rotary kernel moves per access for this call: 8, 4 or
-// 1 (host only; the launcher's rule).
-int rotary_vector_width(const RotaryPlan &p, is_dtype dtype, const RotaryPart *parts, int nparts);
+// Elements a lane of the rotary kernel moves per access: 16 bytes, 8 or one
+// element (host only; the launcher's rule).
+int rotary_vector_width(const RotaryPlan &p, is_dtype dtype);
 // Blocks of 256 threads that one part takes (host only; the launcher's rule).
-int64_t rotary_blocks(const RotaryPlan &p, is_dtype dtype, int vec, const is_tokens &t);
+int64_t rotary_blocks(const RotaryPlan &p, int vec, const is_tokens &t);
 
 struct AttentionPlan {
   cross_attention_desc d;

@@ -5,16 +5,24 @@
 //   or (x - mean) / sqrt(var + eps) over the head's d elements.
 //
 // Every element is read once and written once, so the kernel is bound by
-// memory. A head belongs to `lanes` neighbouring lanes (a power of two); a
-// lane holds both elements of its pairs, so that a pair turns in one lane and
-// only the norm's sum crosses lanes:
-//   half layout:        lane t has the V-element chunks t and t + rot / 2 / V,
-//                       the pairs V t .. V t + V - 1; lanes past the rotated
-//                       part take two neighbouring chunks each and pass them on;
-//   interleaved layout: lane t has the chunks 2t and 2t + 1, the same pairs.
-// V = 8 (16-bit) or 4 (fp32) elements are 16 bytes. Shapes, strides or a
-// rotated part that those chunks do not divide run with V = 4 (16-bit) or 1.
-// A thread's sines serve all the heads it walks over (`slots` apart).
+// memory. A head belongs to 2^log_lanes neighbouring lanes; a lane holds both
+// elements of its pairs, so that a pair turns in one lane and only the norm's
+// sum crosses lanes:
+//   half layout:        the lanes of the turning part have the V elements at
+//                       V t of either half, the pairs V t .. V t + V - 1; the
+//                       lanes after them take two neighbouring chunks each of
+//                       what passes through;
+//   interleaved layout: lane t has the chunks t and t + 2^log_lanes, V / 2 whole
+//                       pairs in each (single elements: 2t and 2t + 1).
+// V elements are 16 bytes, wherever they start: a half or a rest that V does not
+// divide ends in a chunk that reaches back over its neighbour's elements (all
+// loads of a wave's heads come before their stores, and both lanes store the
+// same values). Parts shorter than a chunk run with fewer elements per access.
+//
+// All that a thread needs first (its elements of up to kHeadsAhead heads, the
+// position, the frequencies, the norm's weights) is asked for at once, in vector
+// loads and without branches, so one trip to memory starts a thread's work. A
+// thread's sines serve all the heads it walks over.
 //
 // The angle is formed in turns in 64 bits, the whole turns are dropped there,
 // and only the rest is rounded to 32 bits: error 2^-26 turns at any position.
@@ -48,12 +56,21 @@ struct Args {
   int log_lanes;            // lanes of a head
   int norm;
   float eps, magnitude;
-  double turns[IS_MAX_HEAD_DIM / 2];
+  double turns[IS_MAX_HEAD_DIM / 2];   // of every pair
 };
 
-// Sum over the 2^log_lanes lanes of a head.
+// Sum over the 2^log_lanes lanes of a head: after each step the lanes joined so
+// far hold one value, so that mirrors serve as exchanges of 4 and 8.
 __device__ __forceinline__ float head_sum(float v, int log_lanes) {
-  for (int i = 0; i < log_lanes; ++i) v += __shfl_xor(v, 1 << i);
+  auto add = [&](auto ctrl) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  if (log_lanes > 0) add(std::integral_constant<int, 0xB1>{});    // quad_perm [1, 0, 3, 2]
+  if (log_lanes > 1) add(std::integral_constant<int, 0x4E>{});    // quad_perm [2, 3, 0, 1]
+  if (log_lanes > 2) add(std::integral_constant<int, 0x141>{});   // row_half_mirror
+  if (log_lanes > 3) add(std::integral_constant<int, 0x140>{});   // row_mirror
+  if (log_lanes > 4) v += __shfl_xor(v, 16);
+  if (log_lanes > 5) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -69,9 +86,11 @@ __device__ __forceinline__ void sine(double turns, float &s, float &c) {
 }
 
 // NP: pair groups a lane holds (2 only for V = 1, where 64 lanes may be too few).
-template <typename T, bool HALF, int V, int NP>
+template <typename T, bool HALF, int V, int NP, bool NORM>
 __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
   typedef T vec __attribute__((ext_vector_type(V)));
+  typedef T uvec __attribute__((ext_vector_type(V), aligned(sizeof(T))));   // at any element
+  typedef float fvec __attribute__((ext_vector_type(V), aligned(4)));
   const int which = a.nparts == 2 && blockIdx.x >= a.part[1].first;
   const Part &p = a.part[which];
   const unsigned bid = blockIdx.x - p.first;
@@ -79,57 +98,90 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
   const int lane = threadIdx.x & ((1 << a.log_lanes) - 1);
   const int64_t g = (int64_t)(bid - b * p.blocks) * (kThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
   const int slot = (int)(g & ((1 << p.log_slots) - 1));
-  const int64_t token = g >> p.log_slots;
   // Threads past the last token stay for the lane sums and touch no memory.
-  const bool live = token < p.len;
-  const int chunks = a.d / V, turning = a.rot / 2 / V;
+  const bool live = (g >> p.log_slots) < p.len;
+  const int64_t token = live ? g >> p.log_slots : 0;
+  const int pairs = a.rot / 2, rest = a.d - a.rot, turning = (pairs + V - 1) / V;
 
-  int c0[NP], c1[NP];
+  int at0[NP], at1[NP];     // first element of the lane's two chunks
+  int own0[NP], own1[NP];   // the first of each that is not also another lane's
+  int first[NP], mid[NP];   // pairs of the first chunk; interleaved: of the second
   bool v0[NP], v1[NP];
-  float sn[NP][V], cs[NP][V], w0[NP][V], w1[NP][V];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int t = lane + (i << a.log_lanes);
-    const bool turns = HALF && t < turning;
-    c0[i] = turns ? t : HALF ? 2 * turning + 2 * (t - turning) : 2 * t;
-    c1[i] = turns ? t + turning : c0[i] + 1;
-    v0[i] = live && c0[i] < chunks;
-    v1[i] = live && c1[i] < chunks;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int pair = V * t + j;
-      sn[i][j] = 0.f;
-      cs[i][j] = 1.f;
-      if (live && 2 * pair < a.rot) {
-        const int axis = (pair >= a.per_axis) + (pair >= 2 * a.per_axis);
-        const int32_t pos = p.positions[b * p.pos_b + token * a.axes + axis];
-        sine<T>((double)pos * a.turns[pair - axis * a.per_axis], sn[i][j], cs[i][j]);
-        sn[i][j] *= a.magnitude;
-        cs[i][j] *= a.magnitude;
-      }
-      w0[i][j] = w1[i][j] = 1.f;
-      if (a.norm && p.weight) {
-        if (v0[i]) w0[i][j] = p.weight[c0[i] * V + j];
-        if (v1[i]) w1[i][j] = p.weight[c1[i] * V + j];
-      }
+    if constexpr (HALF) {
+      const bool turns = t < turning;
+      const int u0 = 2 * (t - turning) * V, u1 = u0 + V;    // in what passes through
+      first[i] = mid[i] = turns ? min(V * t, pairs - V) : pairs;
+      at0[i] = turns ? first[i] : a.rot + min(u0, rest - V);
+      at1[i] = turns ? first[i] + pairs : a.rot + min(u1, rest - V);
+      own0[i] = turns ? V * t - first[i] : u0 - (at0[i] - a.rot);
+      own1[i] = turns ? own0[i] : u1 - (at1[i] - a.rot);
+      v0[i] = live && (turns || u0 < rest);
+      v1[i] = live && (turns || u1 < rest);
+    } else {
+      at0[i] = V > 1 ? V * t : 2 * t;
+      at1[i] = V > 1 ? at0[i] + (V << a.log_lanes) : at0[i] + 1;
+      first[i] = at0[i] / 2;
+      mid[i] = at1[i] / 2;
+      own0[i] = own1[i] = 0;
+      v0[i] = live && at0[i] < a.d;
+      v1[i] = live && at1[i] < a.d;
     }
   }
 
   const T *x = static_cast<const T *>(p.x) + b * p.xb + token * p.xt;
   T *y = static_cast<T *>(p.y) + b * p.yb + token * p.yt;
-  const float inv_d = 1.f / (float)a.d;
   const int slots = 1 << p.log_slots;
-  for (int h0 = slot; h0 < p.heads; h0 += kHeadsAhead * slots) {
-    vec r0[kHeadsAhead][NP], r1[kHeadsAhead][NP];
+  vec r0[kHeadsAhead][NP], r1[kHeadsAhead][NP];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kHeadsAhead; ++k)
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int h = h0 + k * slots;
         r0[k][i] = r1[k][i] = vec{};
-        if (h < p.heads && v0[i]) r0[k][i] = *reinterpret_cast<const vec *>(x + h * p.xh + c0[i] * V);
-        if (h < p.heads && v1[i]) r1[k][i] = *reinterpret_cast<const vec *>(x + h * p.xh + c1[i] * V);
+        if (h < p.heads && v0[i]) r0[k][i] = *reinterpret_cast<const uvec *>(x + h * p.xh + at0[i]);
+        if (h < p.heads && v1[i]) r1[k][i] = *reinterpret_cast<const uvec *>(x + h * p.xh + at1[i]);
       }
+  };
+  load(slot);
+
+  float sn[NP][V], cs[NP][V];
+  fvec w0[NP], w1[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    w0[i] = w1[i] = fvec(1.f);
+    if (NORM && p.weight) {
+      if (v0[i]) w0[i] = *reinterpret_cast<const fvec *>(p.weight + at0[i]);
+      if (v1[i]) w1[i] = *reinterpret_cast<const fvec *>(p.weight + at1[i]);
+    }
+  }
+  if (a.rot > 0) {
+    const int32_t *pos = p.positions + b * p.pos_b + token * a.axes;
+    const int32_t q0 = pos[0], q1 = a.axes > 1 ? pos[1] : 0, q2 = a.axes > 2 ? pos[2] : 0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      // Half layout: V pairs from first; interleaved: V / 2 from first and from mid.
+      constexpr int N = HALF || V == 1 ? V : V / 2;
+      typedef double dvec __attribute__((ext_vector_type(N), aligned(8)));
+      const dvec f0 = *reinterpret_cast<const dvec *>(a.turns + min(first[i], IS_MAX_HEAD_DIM / 2 - N));
+      const dvec f1 = *reinterpret_cast<const dvec *>(a.turns + min(mid[i], IS_MAX_HEAD_DIM / 2 - N));
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int pair = j < N ? first[i] + j : mid[i] + j - N;
+        const double f = j < N ? f0[j % N] : f1[j % N];
+        const int32_t q = pair < a.per_axis ? q0 : pair < 2 * a.per_axis ? q1 : q2;
+        sine<T>((double)q * f, sn[i][j], cs[i][j]);
+        sn[i][j] *= a.magnitude;
+        cs[i][j] *= a.magnitude;
+      }
+    }
+  }
+
+  const float inv_d = 1.f / (float)a.d;
+  for (int h0 = slot; h0 < p.heads;) {
 #pragma unroll
     for (int k = 0; k < kHeadsAhead; ++k) {
       const int h = h0 + k * slots;
@@ -141,28 +193,31 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
           e0[i][j] = (float)r0[k][i][j];
           e1[i][j] = (float)r1[k][i][j];
         }
-      if (a.norm) {
-        if (a.norm == IS_NORM_LAYER) {
+      if constexpr (NORM) {
+        // Each element once: not in a chunk that does not exist, nor in the part
+        // of one that belongs to its neighbour.
+        auto sum_own = [&](auto f) {
           float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < NP; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum += e0[i][j] + e1[i][j];
-          const float mean = head_sum(sum, a.log_lanes) * inv_d;
+            for (int j = 0; j < V; ++j) {
+              sum += v0[i] && j >= own0[i] ? f(e0[i][j]) : 0.f;
+              sum += v1[i] && j >= own1[i] ? f(e1[i][j]) : 0.f;
+            }
+          return head_sum(sum, a.log_lanes) * inv_d;
+        };
+        if (a.norm == IS_NORM_LAYER) {
+          const float mean = sum_own([](float v) { return v; });
 #pragma unroll
           for (int i = 0; i < NP; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-              e0[i][j] = v0[i] ? e0[i][j] - mean : 0.f;   // chunks that do not exist stay 0
-              e1[i][j] = v1[i] ? e1[i][j] - mean : 0.f;
+              e0[i][j] -= mean;
+              e1[i][j] -= mean;
             }
         }
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j) sq += e0[i][j] * e0[i][j] + e1[i][j] * e1[i][j];
-        const float inv = 1.f / sqrtf(head_sum(sq, a.log_lanes) * inv_d + a.eps);
+        const float inv = __builtin_amdgcn_rsqf(sum_own([](float v) { return v * v; }) + a.eps);
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
@@ -176,13 +231,14 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
       for (int i = 0; i < NP; ++i) {
         vec o0, o1;
         if constexpr (HALF) {
+          const bool turns = first[i] < pairs;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            o0[j] = (T)(e0[i][j] * cs[i][j] - e1[i][j] * sn[i][j]);
-            o1[j] = (T)(e0[i][j] * sn[i][j] + e1[i][j] * cs[i][j]);
+            o0[j] = (T)(turns ? e0[i][j] * cs[i][j] - e1[i][j] * sn[i][j] : e0[i][j]);
+            o1[j] = (T)(turns ? e0[i][j] * sn[i][j] + e1[i][j] * cs[i][j] : e1[i][j]);
           }
         } else {
-          float e[2 * V], f[2 * V];
+          float e[2 * V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             e[j] = e0[i][j];
@@ -190,19 +246,23 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
           }
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            f[2 * j] = e[2 * j] * cs[i][j] - e[2 * j + 1] * sn[i][j];
-            f[2 * j + 1] = e[2 * j] * sn[i][j] + e[2 * j + 1] * cs[i][j];
+            const bool turns = (V == 1 || j < V / 2 ? first[i] + j : mid[i] + j - V / 2) < pairs;
+            const float u = e[2 * j], v = e[2 * j + 1];
+            e[2 * j] = turns ? u * cs[i][j] - v * sn[i][j] : u;
+            e[2 * j + 1] = turns ? u * sn[i][j] + v * cs[i][j] : v;
           }
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            o0[j] = (T)f[j];
-            o1[j] = (T)f[V + j];
+            o0[j] = (T)e[j];
+            o1[j] = (T)e[V + j];
           }
         }
-        if (v0[i]) *reinterpret_cast<vec *>(y + h * p.yh + c0[i] * V) = o0;
-        if (v1[i]) *reinterpret_cast<vec *>(y + h * p.yh + c1[i] * V) = o1;
+        if (v0[i]) *reinterpret_cast<uvec *>(y + h * p.yh + at0[i]) = o0;
+        if (v1[i]) *reinterpret_cast<uvec *>(y + h * p.yh + at1[i]) = o1;
       }
     }
+    h0 += kHeadsAhead * slots;
+    if (h0 < p.heads) load(h0);
   }
 }
 
@@ -215,21 +275,21 @@ int ceil_log2(int64_t v) {
 // Lanes of a head (log2): those of the pairs, plus one for every two chunks
 // that pass through; V = 1 folds more than 64 onto 64 lanes.
 int log_lanes(const RotaryPlan &p, int vec) {
-  const int chunks = p.d.d / vec;
-  const int turning = p.d.layout == IS_ROTARY_HALF ? p.d.rot / 2 / vec : 0;
-  const int need = turning + (chunks - 2 * turning + 1) / 2;
+  const int turning = (p.d.rot / 2 + vec - 1) / vec, rest = (p.d.d - p.d.rot + vec - 1) / vec;
+  const int need = p.d.layout == IS_ROTARY_HALF ? turning + (rest + 1) / 2 : (p.d.d / vec + 1) / 2;
   const int l = ceil_log2(need);
   return l > 6 ? 6 : l;
 }
 
-// Groups of lanes a token's heads are dealt to (log2). Few tokens: a group per
-// head. Once every CU has 1024 threads that way, groups of up to
-// kHeadsAhead heads, whose sines are then computed once.
+// Groups of lanes a token's heads are dealt to (log2). A group walks up to
+// kHeadsAhead heads, whose loads are in flight together and whose sines are
+// computed once, as long as that leaves every CU 512 threads (64 KB of loads in
+// flight at four heads of two chunks each); few tokens get a group per head.
 int log_slots(const RotaryPlan &p, int vec, const is_tokens &t) {
-  const int l = ceil_log2(t.heads);
-  const double threads = (double)t.n * t.len * (double)((int64_t)1 << (l + log_lanes(p, vec)));
-  const int few = ceil_log2(kHeadsAhead);
-  return threads < 256.0 * 1024 * kHeadsAhead ? l : (l > few ? l - few : 0);
+  int l = ceil_log2(t.heads);
+  const double lanes = (double)t.n * t.len * (double)((int64_t)1 << log_lanes(p, vec));
+  for (int h = 1; h < kHeadsAhead && l > 0 && lanes * (double)((int64_t)1 << (l - 1)) >= 256.0 * 512; h *= 2) --l;
+  return l;
 }
 
 int64_t blocks_per_entry(const RotaryPlan &p, int vec, const is_tokens &t) {
@@ -242,34 +302,36 @@ bool none(const is_tokens &t) { return t.n == 0 || t.len == 0 || t.heads == 0; }
 
 template <typename T, int V, int NP>
 hipError_t launch_t(bool half, const Args &a, unsigned blocks, hipStream_t s) {
-  return half ? launch_kernel(is_k10_rotary<T, true, V, NP>, dim3(blocks), dim3(kThreads), 0, s, a)
-              : launch_kernel(is_k10_rotary<T, false, V, NP>, dim3(blocks), dim3(kThreads), 0, s, a);
+  const dim3 g(blocks), t(kThreads);
+  if (half)
+    return a.norm ? launch_kernel(is_k10_rotary<T, true, V, NP, true>, g, t, 0, s, a)
+                  : launch_kernel(is_k10_rotary<T, true, V, NP, false>, g, t, 0, s, a);
+  return a.norm ? launch_kernel(is_k10_rotary<T, false, V, NP, true>, g, t, 0, s, a)
+                : launch_kernel(is_k10_rotary<T, false, V, NP, false>, g, t, 0, s, a);
 }
 
 }  // namespace
 
-int rotary_vector_width(const RotaryPlan &p, is_dtype dtype, const RotaryPart *parts, int nparts) {
-  for (int v = dtype == IS_F32 ? 4 : 8; v > 1; v /= 2) {
-    if (v == 2) break;   // 8-byte chunks at least, or single elements
-    bool ok = p.d.d % v == 0 && (p.d.layout == IS_ROTARY_INTERLEAVED || p.d.rot / 2 % v == 0);
-    for (int i = 0; i < nparts && ok; ++i)
-      for (const is_tokens *t : {&parts[i].xt, &parts[i].yt}) {
-        if (none(*t)) continue;
-        ok = ok && (t->n == 1 || t->batch_stride % v == 0) && (t->len == 1 || t->token_stride % v == 0) &&
-             (t->heads == 1 || t->head_stride % v == 0);
-      }
+// 16 bytes where the head's parts are at least that long (half layout) or made
+// of such chunks (interleaved), else 8, else single elements. Alignment and
+// strides do not matter: the memory path takes a vector at any element.
+int rotary_vector_width(const RotaryPlan &p, is_dtype dtype) {
+  const int pairs = p.d.rot / 2, rest = p.d.d - p.d.rot;
+  for (int v = dtype == IS_F32 ? 4 : 8; v >= 4; v /= 2) {
+    const bool ok = p.d.layout == IS_ROTARY_HALF ? (pairs == 0 || pairs >= v) && (rest == 0 || rest >= v)
+                                                 : p.d.d % v == 0;
     if (ok) return v;
   }
   return 1;
 }
 
-int64_t rotary_blocks(const RotaryPlan &p, is_dtype, int vec, const is_tokens &t) {
+int64_t rotary_blocks(const RotaryPlan &p, int vec, const is_tokens &t) {
   return none(t) ? 0 : t.n * blocks_per_entry(p, vec, t);
 }
 
 hipError_t launch_rotary(const RotaryPlan &p, is_dtype dtype, int norm, float eps, const RotaryPart *parts,
                          int nparts, hipStream_t s) {
-  const int vec = rotary_vector_width(p, dtype, parts, nparts);
+  const int vec = rotary_vector_width(p, dtype);
   Args a;
   a.nparts = 0;
   a.d = p.d.d;
