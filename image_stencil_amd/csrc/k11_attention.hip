@@ -891,6 +891,46 @@ hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
 
 }  // namespace
 
+// How a call is cut, by an estimate of its time in microseconds fitted to runs of
+// 1024 and 4096 keys with 9 entries x heads of 1021 to 4000 queries, heads of 32 to 256
+// (within 15%; what all choices share, the read of k and v, is left out):
+//   shared tiles, 128 rows a workgroup, a step of 64 keys: 0.50 + dp / 350 alone
+//     on its CU, 0.70 + dp / 140 for two (heads of 64: 0.68 and 1.1 measured; of
+//     128: 0.86 and 1.5); heads over 128 leave LDS for one, 0.1 + dp / 140;
+//   own tiles, 32 rows, a step of 32 keys a wave: 0.60 + dp / 500 (heads of 96:
+//     0.75 measured) alone, half as much again for two (heads to 64);
+//   start and end: 5 + dp / 32 (shared), 5 + dp / 64 (own);
+//   joining splits: 1.5, and their 32-bit results written and read at 4 TB/s.
+// E.g. 2042 rows x 9 heads of 96 over 1543 keys: shared, no splits, 27.4 us; three
+// splits 33.2; own tiles 43.8. 800 rows: own tiles 16.9; shared in two 21.9.
+struct Cut {
+  bool few;
+  int splits, split_keys;
+  double us;
+};
+
+Cut estimate(const AttentionPlan &p, bool few, int64_t splits) {
+  const cross_attention_desc &d = p.d;
+  const int step = few ? 32 * few_waves(p.dp) : 64;
+  const int64_t heads = (int64_t)d.n * d.hkv;
+  const int64_t units = heads * ((p.rows + (few ? 31 : 127)) / (few ? 32 : 128));
+  int64_t keys = ((d.lk + splits - 1) / splits + step - 1) / step * step;
+  if (keys < step) keys = step;
+  Cut c = {few, (int)((d.lk + keys - 1) / keys), (int)keys, 0.0};
+  if (c.splits < 1) c.splits = 1;
+  const int64_t blocks = units * c.splits;
+  const bool pairs = few ? p.dp <= 64 : p.dp <= 128;      // two workgroups on a CU
+  const double one = few ? 0.6 + p.dp / 500.0 : pairs ? 0.5 + p.dp / 350.0 : 0.1 + p.dp / 140.0;
+  const double two = few ? 1.5 * one : 0.7 + p.dp / 140.0;
+  const int64_t round = pairs ? 512 : 256;
+  const int64_t rest = blocks % round;
+  const double per_step = (double)(blocks / round) * (pairs ? two : one) +
+                          (rest == 0 ? 0.0 : rest > 256 ? two : one);
+  c.us = 5.0 + p.dp / (few ? 64.0 : 32.0) + (double)(keys / step) * per_step;
+  if (c.splits > 1) c.us += 1.5 + 8.0 * (double)heads * p.rows * c.splits * d.d / 4.0e6;
+  return c;
+}
+
 bool configure_attention(AttentionPlan &p) {
   const cross_attention_desc &d = p.d;
   p.group = d.hq / d.hkv;
@@ -898,29 +938,29 @@ bool configure_attention(AttentionPlan &p) {
   p.dp = kHeads[0];
   for (const int h : kHeads)
     if (p.dp < d.d) p.dp = h;
-  const bool few = p.rows <= 32;
+  Cut best = estimate(p, p.rows <= 32, 1);
+  for (int kind = 0; kind < 2; ++kind)
+    for (int64_t splits = 1; splits <= 128 && splits * 128 <= d.lk + 127; splits += splits < 16 ? 1 : splits / 8) {
+      if (kind == 1 && p.rows <= 32) break;   // a shared tile would leave waves without rows
+      const Cut c = estimate(p, kind == 0, splits);
+      if (c.us < best.us) best = c;
+    }
+  const bool few = best.few;
   p.name = few ? "is_k11_attention_few" : "is_k11_attention";
   p.tile_rows = few ? 32 : 128;
   p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   p.block = few ? 64 * few_waves(p.dp) : 256;
   p.units = (int64_t)d.n * d.hkv * p.row_tiles;
-  const int tile = few ? 32 * few_waves(p.dp) : 64;
-  const int slots = few ? 256 : 512;
-  const int64_t most = d.lk / (few ? 512 : 256);
-  int64_t splits = p.units > 0 ? slots / p.units : 1;
-  splits = splits < most ? splits : most;
-  splits = splits > 1 ? splits : 1;
-  p.split_keys = (int)(((d.lk + splits - 1) / splits + tile - 1) / tile * tile);
-  if (p.split_keys < tile) p.split_keys = tile;
-  p.splits = (int)((d.lk + (int64_t)p.split_keys - 1) / p.split_keys);
-  if (p.splits < 1) p.splits = 1;
+  p.splits = best.splits;
+  p.split_keys = best.split_keys;
   // Few keys and many row tiles: a workgroup keeps the keys for several, which
   // leaves one round of workgroups. (One tile each: the trip to memory, the
-  // products and the stores of one row tile follow each other in every workgroup.)
+  // products and the stores of one row tile follow each other in every workgroup;
+  // 8 x 4096 rows x 8 heads of 40 over 120 keys: 25.8 us against 18.4.)
   const int kept = p.dp <= 64 ? 4 : 2;   // tiles that fit the buffers
   p.run = 1;
   if (!few && p.splits == 1 && p.dp <= kResidentHead && d.lk <= kept * 64) {
-    const int64_t run = p.units / slots;
+    const int64_t run = p.units / 512;
     p.run = (int)(run < 1 ? 1 : run > p.row_tiles ? p.row_tiles : run);
   }
   return p.units * p.splits <= 2147483647;
