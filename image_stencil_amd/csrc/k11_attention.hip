@@ -241,39 +241,46 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     koff[i] = kc * 8 < a.d ? (unsigned)(r * ktok + kc * 16) : kOob;
     voff[i] = vc * 8 < a.d ? (unsigned)(r * vtok + vc * 16) : kOob;
   }
-  // Rows of a tile at `key` that may be seen; a tile past the keys gets zeros.
-  auto issue = [&](const char *base, int tok, const unsigned *off, int key, unsigned dst, uint64_t bits) {
-    const int left = min(keys - key, KT);
-    const uintx4 rs = descriptor((uint64_t)(uintptr_t)base + (uint64_t)((int64_t)key * tok),
-                                 left > 0 ? (unsigned)((left - 1) * tok + a.d * 2) : 0u);
-    auto all = [&](auto whole) {
-      unsigned o[NI];
+  // The next K or V tile into LDS at dst: its rows that may be seen; a tile past
+  // the keys gets zeros. The descriptor spans a whole tile: rows that may not be
+  // read have an offset outside it.
+  uint64_t knext = (uint64_t)(uintptr_t)kbase + (uint64_t)((int64_t)tile_key(0) * ktok);
+  uint64_t vnext = (uint64_t)(uintptr_t)vbase + (uint64_t)((int64_t)tile_key(0) * vtok);
+  const int stride = SHARED ? KT : NW * KT;   // keys from one of this wave's tiles to the next
+  const uint64_t kstep = (uint64_t)((int64_t)stride * ktok), vstep = (uint64_t)((int64_t)stride * vtok);
+  const unsigned kspan = (unsigned)((KT - 1) * ktok + a.d * 2), vspan = (unsigned)((KT - 1) * vtok + a.d * 2);
+  auto issue = [&](uint64_t &at, uint64_t step, unsigned span, const unsigned *off, int left, unsigned dst,
+                   uint64_t bits) {
+    const uintx4 rs = descriptor(at, span);
+    at += step;
+    unsigned o[NI];
+    if constexpr (MASK) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if constexpr (decltype(whole)::value) {
-          o[i] = off[i];
-        } else if constexpr (MASK) {
-          // All ones where the row's bit is set: one bit-field extract and one select.
-          constexpr int SPAN = G::LOADERS * 64 / CP;   // rows of an operation
-          const int r = drow[i];
-          const bool low = KT == 32 || (SPAN <= 32 ? i * SPAN < 32 : r < 32);
-          const int word = low ? (int)bits : (int)(bits >> 32);
-          const unsigned m = (unsigned)__builtin_amdgcn_sbfe(word, (unsigned)(r & 31), 1);
-          o[i] = (off[i] & m) | (kOob & ~m);
-        } else {
-          o[i] = drow[i] < left ? off[i] : kOob;
-        }
+        // All ones where the row's bit is set: one bit-field extract and one select.
+        constexpr int SPAN = G::LOADERS * 64 / CP;   // rows of an operation
+        const int r = drow[i];
+        const bool low = KT == 32 || (SPAN <= 32 ? i * SPAN < 32 : r < 32);
+        const int word = low ? (int)bits : (int)(bits >> 32);
+        const unsigned m = (unsigned)__builtin_amdgcn_sbfe(word, (unsigned)(r & 31), 1);
+        o[i] = (off[i] & m) | (kOob & ~m);
       }
+    } else if (left < KT) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) o[i] = drow[i] < left ? off[i] : kOob;
       dma16<NI, G::LOADERS * 1024>(rs, dst + (SHARED ? wave : 0) * 1024u, o);
-    };
-    if (MASK ? !~(bits | (KT == 64 ? 0 : ~(uint64_t)0 << (KT & 63))) : left == KT) all(std::true_type{});
-    else all(std::false_type{});
+      return;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) o[i] = off[i];
+    }
+    dma16<NI, G::LOADERS * 1024>(rs, dst + (SHARED ? wave : 0) * 1024u, o);
   };
-  auto issue_k = [&](int j, int buffer, uint64_t bits) {
-    issue(kbase, ktok, koff, tile_key(j), ring_at + buffer * G::TILE, bits);
+  auto issue_k = [&](int j, int buffer, uint64_t bits) {   // tiles in order
+    issue(knext, kstep, kspan, koff, keys - tile_key(j), ring_at + buffer * G::TILE, bits);
   };
   auto issue_v = [&](int j, int buffer, uint64_t bits) {
-    issue(vbase, vtok, voff, tile_key(j), ring_at + (RB + buffer) * G::TILE, bits);
+    issue(vnext, vstep, vspan, voff, keys - tile_key(j), ring_at + (RB + buffer) * G::TILE, bits);
   };
   // At most N of this wave's DMA operations still out, then (a shared tile)
   // every wave's.
@@ -285,26 +292,31 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     if constexpr (SHARED) __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
   };
-  // Mask bytes of tile j: the words that hold them, into slot j % 4. The words'
-  // other bytes belong to the same aligned word and are dropped (seen).
+  // Mask bytes: the words from tile j's first on, into slot j % 4 (tiles in order).
+  // The descriptor ends with the word of the last key; a first word may begin with
+  // up to three bytes before it.
   const unsigned masks_at = lds_at + (unsigned)(G::MASKS + wave * G::MASK_WAVE);
   const uint64_t mask0 = MASK ? (uint64_t)(uintptr_t)a.mask + (uint64_t)(b * a.mask_bs + first) : 0;
+  const int skip = (int)(mask0 & 3);
+  const uintx4 mask_rs = descriptor(mask0 & ~(uint64_t)3, (unsigned)((keys + skip + 3) & ~3));
+  unsigned mask_off = (unsigned)(tile_key(0) + lane * 4);
   auto issue_mask = [&](int j) {
     if constexpr (MASK) {
-      const uint64_t at = mask0 + (uint64_t)tile_key(j);
-      const int left = min(keys - tile_key(j), KT), skip = (int)(at & 3);
-      const uintx4 rs = descriptor(at & ~(uint64_t)3, left > 0 ? (unsigned)((left + skip + 3) & ~3) : 0u);
-      dma4(rs, masks_at + (unsigned)(j % G::MASK_SLOTS) * G::MASK_SLOT, lane * 4u);
+      dma4(mask_rs, masks_at + (unsigned)(j & (G::MASK_SLOTS - 1)) * G::MASK_SLOT, mask_off);
+      mask_off += (unsigned)stride;
     }
   };
-  // A bit for every key of tile j that may be seen.
-  auto seen = [&](int j) -> uint64_t {
+  // A bit for every key of tile j that may be seen; its two parts, the read of a
+  // byte per lane and the vote, may stand apart.
+  auto mask_byte = [&](int j) -> uint8_t {
     if constexpr (!MASK) return 0;
-    const int key = tile_key(j);
-    const int skip = (int)((mask0 + (uint64_t)key) & 3);
-    const uint8_t byte = lds[G::MASKS + wave * G::MASK_WAVE + j % G::MASK_SLOTS * G::MASK_SLOT + skip + lane % KT];
-    return __ballot(lane < KT && key + lane < keys && byte != 0);
+    return (uint8_t)lds[G::MASKS + wave * G::MASK_WAVE + (j & (G::MASK_SLOTS - 1)) * G::MASK_SLOT + skip + lane % KT];
   };
+  auto vote = [&](int j, uint8_t byte) -> uint64_t {
+    if constexpr (!MASK) return 0;
+    return __ballot(lane < KT && tile_key(j) + lane < keys && byte != 0);
+  };
+  auto seen = [&](int j) -> uint64_t { return vote(j, mask_byte(j)); };
 
   // ---- Queries: B operands, lane = row n32, elements 16 kk + 8 half .. + 7.
   T8 qf[QB][KK];
@@ -371,7 +383,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   };
   auto set_bias = [&](int slot, uint64_t bits) {   // of a tile: slot tile % 2
     if constexpr (MASK) {
-      if (lane < KT) bias[slot * KT + lane] = (bits >> lane) & 1 ? 0.f : -INFINITY;
+      if (lane < KT) bias[slot * KT + lane] = __builtin_amdgcn_inverse_ballot_w64(bits) ? 0.f : -INFINITY;
     }
   };
   // The largest score of every row, in M's unit; half of the lanes' maximum
@@ -447,9 +459,10 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   // A slot is one A operand's products and what the vector unit does in their 32
   // cycles each; the fences keep the order, since a wave issues in order and the
   // compiler would put each kind in a run of its own. Operands are read kAhead
-  // slots early. k_done() follows the last use of the K tile, v_here() precedes
-  // the first read of the V tile.
-  auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top, auto k_done, auto v_here) {
+  // slots early. v_here() precedes the first read of the V tile; beside(slot) is
+  // what a slot carries of the loads to come (the scalar work of a descriptor
+  // takes as long as a product).
+  auto step = [&](auto buffer, auto next, const Scores &s, Scores &n, float *top, auto v_here, auto beside) {
     const int B = buffer;   // a constant where the loop is unrolled
     constexpr int NEXT = decltype(next)::value;
     constexpr int FIRST = NEXT ? 0 : F_K, SLOTS = F_K + F_V;
@@ -496,7 +509,6 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     static_for<SLOTS - FIRST>([&](auto i) {
       constexpr int U = FIRST + decltype(i)::value;
       if constexpr (!EARLY && U + kAhead == F_K) v_here();
-      if constexpr (NEXT && U == F_K) k_done();
       fetch(std::integral_constant<int, U + kAhead>{});
       const T8 x = op[U % (kAhead + 1)];
       if constexpr (U < F_K) {
@@ -535,6 +547,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
           pin(sum[qb][1]);
         }
       }
+      if constexpr (NEXT) beside(std::integral_constant<int, U>{});
       __builtin_amdgcn_sched_barrier(0);
     });
 #pragma unroll
@@ -569,7 +582,7 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     constexpr int SP = G::SP;
     int j = 0;
     uint64_t bits[SP + 1] = {};   // of tiles j + SP .. j + 2 SP; own tiles: bits[0] of j + 2
-    auto none = [] {};
+    auto none = [](auto...) {};
     // Scores of tile j + 1 into n beside the rest of tile j; u = j % RB.
     auto advance = [&](auto u, const Scores &s, Scores &n) {
       constexpr int B = decltype(u)::value;
@@ -580,30 +593,50 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
           bits[SP == 1 ? 1 : B % SP] = B + 2 < RB ? early[B + 2] : 0;
         } else if constexpr (B % SP == 0) {
           arrived(std::integral_constant<int, 0>{});
-#pragma unroll
-          for (int i = 0; i <= SP; ++i) bits[i] = seen(j + SP + i);
-#pragma unroll
-          for (int i = 1; i <= SP; ++i) issue_mask(j + 2 * SP + i);
-#pragma unroll
-          for (int i = 0; i < SP; ++i)
-            if (j > 0) issue_v(j + SP + i, (B + SP + i) % RB, bits[i]);
-#pragma unroll
-          for (int i = 1; i <= SP; ++i)
-            if (j > 0 || i == SP) issue_k(j + SP + i, (B + SP + i) % RB, bits[i]);
+          if (MASK && j == 0) bits[SP] = seen(2 * SP);
         }
         set_bias(B % 2, bits[SP == 1 ? 1 : B % SP]);   // of tile j + 2
-        step(u, std::integral_constant<int, 1>{}, s, n, top, none, none);
+        // The next SP tiles' bits: read before the step, voted on after it.
+        constexpr bool VOTE = MASK && !RESIDENT && B % SP == SP - 1;
+        uint8_t bytes[SP];
+        if constexpr (VOTE) {
+#pragma unroll
+          for (int i = 0; i < SP; ++i) bytes[i] = mask_byte(j + SP + 2 + i);
+        }
+        step(u, std::integral_constant<int, 1>{}, s, n, top, none, [&](auto slot) {
+          // In slots 1, 3, ...: V tiles j + SP .., K tiles j + SP + 1 .., the masks.
+          constexpr int U = decltype(slot)::value, I = U / 2;
+          if constexpr (!RESIDENT && B % SP == 0 && U % 2 == 1) {
+            if constexpr (I < SP) {
+              if (j > 0) issue_v(j + SP + I, (B + SP + I) % RB, bits[I]);
+            } else if constexpr (I < 2 * SP) {
+              constexpr int K = I - SP + 1;
+              if (j > 0 || K == SP) issue_k(j + SP + K, (B + SP + K) % RB, bits[K]);
+            }
+            if constexpr (I == 2 * SP - 1) {
+#pragma unroll
+              for (int i = 1; i <= SP; ++i) issue_mask(j + 3 * SP + i);
+            }
+          }
+        });
+        if constexpr (VOTE) {
+          bits[0] = bits[SP];
+#pragma unroll
+          for (int i = 0; i < SP; ++i) bits[1 + i] = vote(j + SP + 2 + i, bytes[i]);
+        }
       } else {
         uint64_t next = 0;
         arrived(std::integral_constant<int, 3 * NI + MASK>{});
         step(u, std::integral_constant<int, 1>{}, s, n, top,
-             [&] {
-               next = seen(j + 3);
-               set_bias((B + 1) % 2, next);
-               issue_mask(j + 5);
-               issue_k(j + 3, (B + 3) % RB, next);
-             },
-             [&] { arrived(std::integral_constant<int, 2 * NI + MASK>{}); });
+             [&] { arrived(std::integral_constant<int, 2 * NI + MASK>{}); },
+             [&](auto slot) {
+               if constexpr (decltype(slot)::value == F_K - 1) {   // the K tile's last use
+                 next = seen(j + 3);
+                 set_bias((B + 1) % 2, next);
+                 issue_mask(j + 5);
+                 issue_k(j + 3, (B + 3) % RB, next);
+               }
+             });
         issue_v(j + 2, B, bits[0]);
         bits[0] = next;
       }
@@ -621,7 +654,12 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
 #pragma unroll
       for (int i = 0; i < RB; ++i) early[i] = seen(i);
       if constexpr (!SHARED) bits[0] = seen(2);
-      else if constexpr (!RESIDENT) issue_mask(RB);
+      else if constexpr (!RESIDENT) {
+#pragma unroll
+        for (int i = 0; i < SP; ++i) bits[i] = early[SP + i];
+#pragma unroll
+        for (int i = 0; i <= SP; ++i) issue_mask(RB + i);
+      }
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i) issue_k(i, i, early[i]);
@@ -671,10 +709,11 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
         }
       });
     }
-    step(j % RB, std::integral_constant<int, 0>{}, s0, s1, top, none,
+    step(j % RB, std::integral_constant<int, 0>{}, s0, s1, top,
          [&] {
            if (!again) arrived(std::integral_constant<int, SHARED ? 0 : 2 * NI>{});
-         });
+         },
+         none);
     // The tiles past the last: LDS is used again below, and by the next workgroup.
     if constexpr (!SHARED) arrived(std::integral_constant<int, 0>{});
   }
@@ -893,7 +932,7 @@ hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
 
 // How a call is cut, by an estimate of its time in microseconds fitted to runs of
 // 1024 and 4096 keys with 9 entries x heads of 1021 to 4000 queries, heads of 32 to 256
-// (within 15%; what all choices share, the read of k and v, is left out):
+// (within 15%), and the read of k and v where that takes longer:
 //   shared tiles, 128 rows a workgroup, a step of 64 keys: 0.50 + dp / 350 alone
 //     on its CU, 0.70 + dp / 140 for two (heads of 64: 0.68 and 1.1 measured; of
 //     128: 0.86 and 1.5); heads over 128 leave LDS for one, 0.1 + dp / 140;
@@ -913,9 +952,11 @@ Cut estimate(const AttentionPlan &p, bool few, int64_t splits) {
   const cross_attention_desc &d = p.d;
   const int step = few ? 32 * few_waves(p.dp) : 64;
   const int64_t heads = (int64_t)d.n * d.hkv;
+  if (p.rows <= 0 || heads <= 0) return {few, 1, step, 0.0};
   const int64_t units = heads * ((p.rows + (few ? 31 : 127)) / (few ? 32 : 128));
-  int64_t keys = ((d.lk + splits - 1) / splits + step - 1) / step * step;
-  if (keys < step) keys = step;
+  const int tile = few ? 32 : 64;
+  int64_t keys = ((d.lk + splits - 1) / splits + tile - 1) / tile * tile;
+  if (keys < tile) keys = tile;
   Cut c = {few, (int)((d.lk + keys - 1) / keys), (int)keys, 0.0};
   if (c.splits < 1) c.splits = 1;
   const int64_t blocks = units * c.splits;
@@ -926,7 +967,10 @@ Cut estimate(const AttentionPlan &p, bool few, int64_t splits) {
   const int64_t rest = blocks % round;
   const double per_step = (double)(blocks / round) * (pairs ? two : one) +
                           (rest == 0 ? 0.0 : rest > 256 ? two : one);
-  c.us = 5.0 + p.dp / (few ? 64.0 : 32.0) + (double)(keys / step) * per_step;
+  const double read = (double)heads * d.lk * d.d * 4.0 / 5.0e6;   // of k and v at 5 TB/s
+  const double walk = (double)((keys + step - 1) / step) * per_step;
+  // The shorter of the two is not quite hidden by the longer.
+  c.us = 5.0 + p.dp / (few ? 64.0 : 32.0) + (walk > read ? walk + read / 4 : read + walk / 4);
   if (c.splits > 1) c.us += 1.5 + 8.0 * (double)heads * p.rows * c.splits * d.d / 4.0e6;
   return c;
 }
