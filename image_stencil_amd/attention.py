@@ -69,8 +69,8 @@ def cross_attention_workspace_size(plan):
 
 
 def cross_attention_get_plan_info(plan):
-    """grid: (row tiles over all heads and entries, parts of the keys, 1); tile:
-    (keys per part, rows per workgroup)."""
+    """grid: (workgroups over all heads and entries, parts of the keys, 1); tile:
+    (keys per part, rows of a row tile)."""
     info = conv2d_plan_info()
     _abi.check(_abi.load().cross_attention_get_plan_info(plan, ctypes.byref(info)), "cross_attention_get_plan_info")
     return {"kernel": info.kernel.decode(), "grid": (info.grid_x, info.grid_y, info.grid_z), "block": info.block,

@@ -300,7 +300,7 @@ is_status cross_attention_get_plan_info(cross_attention_plan plan, conv2d_plan_i
   const cross_attention_desc &d = p.d;
   memset(info, 0, sizeof(*info));
   strncpy(info->kernel, p.name, sizeof(info->kernel) - 1);
-  info->grid_x = (int)p.units;
+  info->grid_x = (int)p.workgroups;
   info->grid_y = p.splits;
   info->grid_z = 1;
   info->block = p.block;

@@ -46,10 +46,11 @@ struct AttentionPlan {
   int tile_rows;          // rows per workgroup
   int row_tiles;
   int splits;             // workgroups the keys of one row tile are split over
-  int split_keys;         // keys per split, a multiple of the key tile
+  int split_keys;         // keys per split, a multiple of a wave's key tile
   int run;                // row tiles a workgroup goes through
   int block, lds;
   int64_t units;          // n * hkv * row_tiles
+  int64_t workgroups;     // of one split: n * hkv * runs of row tiles
 };
 
 // Fills everything after d and scale; false when the grid would be too large.

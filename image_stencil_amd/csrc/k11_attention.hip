@@ -986,11 +986,11 @@ bool configure_attention(AttentionPlan &p) {
   for (int kind = 0; kind < 2; ++kind)
     for (int64_t splits = 1; splits <= 128 && splits * 128 <= d.lk + 127; splits += splits < 16 ? 1 : splits / 8) {
       if (kind == 1 && p.rows <= 32) break;   // a shared tile would leave waves without rows
+      if (splits > 1 && (double)d.n * d.hkv * p.rows * d.d > 2147483647.0) break;   // the joining grid
       const Cut c = estimate(p, kind == 0, splits);
       if (c.us < best.us) best = c;
     }
   const bool few = best.few;
-  p.name = few ? "is_k11_attention_few" : "is_k11_attention";
   p.tile_rows = few ? 32 : 128;
   p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   p.block = few ? 64 * few_waves(p.dp) : 256;
@@ -1007,6 +1007,13 @@ bool configure_attention(AttentionPlan &p) {
     const int64_t run = p.units / 512;
     p.run = (int)(run < 1 ? 1 : run > p.row_tiles ? p.row_tiles : run);
   }
+  p.name = few ? "is_k11_attention (own tiles)" : p.run > 1 ? "is_k11_attention (resident)" : "is_k11_attention";
+  p.workgroups = (int64_t)d.n * d.hkv * ((p.row_tiles + p.run - 1) / p.run);
+  for_head(p.dp, [&](auto dp) {
+    constexpr int DP = decltype(dp)::value;
+    p.lds = few ? Geo<DP, few_waves(DP), false, false>::BYTES : Geo<DP, 4, true, false>::BYTES;
+    return hipSuccess;
+  });
   return p.units * p.splits <= 2147483647;
 }
 
