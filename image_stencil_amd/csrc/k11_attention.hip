@@ -13,19 +13,29 @@
 // read in the same order of keys: P never crosses lanes or LDS. M, l and the
 // factor of a rescale belong to a query, which is a lane.
 //
-// A workgroup of NW waves either shares key tiles of KT keys, 32 QB query rows
-// per wave (SHARED: many queries), or lets every wave walk key tiles of its own
-// for the same 32 rows and joins the waves' results at the end (few queries,
-// where the read of k and v is all the work). K and V arrive by LDS DMA in two
-// buffers each, without passing registers. Step j issues K tile j + 2 and V tile
-// j + 1, computes the scores of tile j + 1 beside the exponentials of tile j
-// (matrix cores beside vector unit), then adds tile j's p v beside the maximum
-// of tile j + 1. M moves only when a row's maximum outgrows it by 2^8, so that
-// most steps scale nothing; p stays under 2^8, exact in what follows.
+// A workgroup of NW waves either shares key tiles of 64 keys, 32 QB query rows
+// per wave (SHARED: many queries; RESIDENT: all keys stay in LDS for several row
+// tiles), or lets every wave walk key tiles of 32 of its own for the same 32 rows
+// and joins the waves' results at the end (few queries, where the read of k and v
+// is all the work). K and V arrive by LDS DMA in two or four buffers each, without
+// passing registers. A step computes the scores of tile j + 1 beside the
+// exponentials of tile j (matrix cores beside vector unit), then adds tile j's p v
+// beside the maximum of tile j + 1, and issues the loads of the tiles after. M
+// moves only when a row's maximum outgrows it by 2^8, so that most steps scale
+// nothing; p stays under 2^8, and its sum in 32 bits.
 //
 // Rows of k and v that may not be seen are never fetched (an out-of-range
 // offset makes the DMA write zeros); their scores start from -infinity, in the
 // accumulator (MASK) or after the product (the last tile's end).
+//
+// What bounds it, measured on one MI355X: heads of 128, 16384 x 16384 tokens, 16
+// query and 4 key heads, bf16: 1868 us, 1.17 PFLOP/s, the rate of a large library
+// product on the same card, at the clock the power limit leaves. Heads of 64,
+// 3600 x 3600, 16 heads, fp16: 74 us, 0.71 PFLOP/s: per 32 x 32 scores the vector
+// unit's 16 exponentials (8 cycles each), multiply-adds, sums, conversions and
+// maxima take about 230 cycles of a wave and the products 256, and one wave's
+// instructions leave it no faster than one in five cycles. One token over
+// 4 x 32771 keys, 2 heads of 128: 30.9 us, 4.3 TB/s of k and v with the join.
 #include <float.h>
 #include <math.h>
 
