@@ -363,10 +363,11 @@ class CrossAttention:
         return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device) if self.workspace_bytes else None
 
     def forward(self, q, k, v, out=None, key_mask=None, key_lengths=None, lse=None, workspace=None, stream=None):
-        """Attention into `out` (None: a new dense tensor). key_mask: bool or
-        uint8, n x lk, true where a key is visible; key_lengths: int32, n; lse:
-        float32, n x hq x lq, receives the log-sum-exp of each row. workspace:
-        from new_workspace() (None: allocated for the call)."""
+        """Attention into `out` (None: a new tensor with the strides of the plan's,
+        dense unless the plan was made for another). key_mask: bool or uint8,
+        n x lk, true where a key is visible; key_lengths: int32, n; lse: float32,
+        n x hq x lq, receives the log-sum-exp of each row. workspace: from
+        new_workspace() (None: allocated for the call)."""
         try:
             key = (_sig(q), _sig(k), _sig(v), _sig(out), _sig(key_mask), _sig(key_lengths), _sig(lse))
             seen = self._layouts.get(key)
@@ -382,7 +383,7 @@ class CrossAttention:
             _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
                           workspace=workspace)
         if out is None:
-            out = self._torch.empty(self._like[3][0], dtype=self.dtype, device=q.device)
+            out = self._torch.empty_strided(*self._like[3], dtype=self.dtype, device=q.device)
         if workspace is None and self.workspace_bytes:
             workspace = self.new_workspace(q.device)
         st = self._lib.cross_attention_forward(self.handle, q.data_ptr() or None, k.data_ptr() or None,

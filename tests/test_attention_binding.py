@@ -1,0 +1,90 @@
+"""What the attention binding hands to the library, on the CPU: tensors that pass
+for device tensors and a library that records its calls in place of launching."""
+import pytest
+import torch
+
+import image_stencil_amd as isa
+from image_stencil_amd import attention
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it lies on GPU `index`."""
+    index = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.index
+
+    __torch_function__ = torch._C._disabled_torch_function_impl
+
+
+def gpu(t, index=0):
+    t = torch.Tensor._make_subclass(OnGpu, t)
+    t.index = index
+    return t
+
+
+class Recorder:
+    """Stands in for the library: every function records its arguments."""
+
+    def __init__(self, on_call=None):
+        self.calls, self.on_call = [], on_call
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            if self.on_call:
+                self.on_call(name, args)
+            return 0
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """One machine with GPUs 0 (current) and 1; current streams 1000 and 1001."""
+    state = {"current": 0}
+
+    class Device:
+        def __init__(self, index):
+            self.index = index.index if isinstance(index, torch.device) else index
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.index
+
+        def __exit__(self, *exc):
+            state["current"] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["current"])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    # Every given tensor passes for one of the same device, allocated ones too.
+    monkeypatch.setattr(attention, "_one_device", lambda tensors: True)
+    return state
+
+
+def _t(*shape, dtype=torch.float16, index=0):
+    return gpu(torch.zeros(shape, dtype=dtype), index)
+
+
+def _span(shape, stride):
+    """Elements from the first to the end of the last."""
+    return 1 + sum((n - 1) * s for n, s in zip(shape, stride))
+
+
+def test_a_missing_output_has_room_for_what_the_plan_writes(fake):
+    """A plan made for a slice of a wider tensor, called without that tensor: the
+    memory that is allocated holds every element the plan's strides reach."""
+    n, lq, heads, d = 2, 5, 4, 64
+    q, k = _t(n, lq, heads, d), _t(n, 7, heads, d)
+    wide = torch.zeros(n, lq, 3 * heads, d, dtype=torch.float16)[:, :, heads:2 * heads]
+    for out in (wide, wide.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3), None):
+        plan = isa.CrossAttention(q, k, k, out)
+        plan._lib = Recorder()
+        got = plan.forward(q, k, k)
+        assert got.shape == q.shape
+        strides = tuple(plan._desc.out_stride) + (1,)
+        room = got.untyped_storage().nbytes() // 2 - got.storage_offset()
+        assert _span(got.shape, strides) <= room, "writes %d elements into %d" % (_span(got.shape, strides), room)
+        assert got.stride() == strides     # and it is read as it was written
+        assert plan._lib.calls[-1][1][6] == got.data_ptr()
