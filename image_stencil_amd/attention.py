@@ -376,6 +376,11 @@ class CrossAttention:
         if not seen:
             self._check_forward(q, k, v, out, key_mask, key_lengths, lse)
             self._layouts.keep(key, True)
+        if workspace is not None:
+            if not isinstance(workspace, self._torch.Tensor):
+                raise TypeError("workspace must be a tensor")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
         if stream is not None and (out is None or (workspace is None and self.workspace_bytes)):
             raise ValueError("a call on a stream of its own needs out and workspace: memory allocated here belongs "
                              "to torch's current stream")

@@ -88,3 +88,22 @@ def test_a_missing_output_has_room_for_what_the_plan_writes(fake):
         assert _span(got.shape, strides) <= room, "writes %d elements into %d" % (_span(got.shape, strides), room)
         assert got.stride() == strides     # and it is read as it was written
         assert plan._lib.calls[-1][1][6] == got.data_ptr()
+
+
+def test_a_workspace_with_gaps_or_repeats_is_refused(fake):
+    """The kernel takes consecutive bytes from the workspace's base, whatever the
+    tensor's strides say: one byte repeated counts as enough, and is not."""
+    q, k = _t(1, 1, 8, 128), _t(1, 40000, 1, 128)
+    plan = isa.CrossAttention(q, k, k)
+    plan._lib = Recorder()
+    need = plan.workspace_bytes
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8)
+    plan.forward(q, k, k, workspace=ws)
+    plan.forward(q, k, k, workspace=torch.zeros((need + 3) // 4, dtype=torch.float32))
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            plan.forward(q, k, k, workspace=bad)
+    with pytest.raises(TypeError, match="workspace"):
+        plan.forward(q, k, k, workspace=need)
+    assert len(plan._lib.calls) == 2
