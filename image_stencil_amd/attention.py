@@ -16,6 +16,7 @@ _LAYOUTS = {"half": _abi.IS_ROTARY_HALF, "interleaved": _abi.IS_ROTARY_INTERLEAV
 _SCALINGS = {"none": _abi.IS_ROTARY_UNSCALED, "linear": _abi.IS_ROTARY_LINEAR, "ntk": _abi.IS_ROTARY_NTK,
              "ramp": _abi.IS_ROTARY_RAMP}
 _NORMS = {"rms": _abi.IS_NORM_RMS, "layer": _abi.IS_NORM_LAYER}
+_ALLOCATED = "memory allocated here belongs to torch's current stream"
 
 
 # ------------------------------------------------------------------ the C names
@@ -224,7 +225,8 @@ class Rotary:
 
     def apply(self, x, positions, out=None, stream=None):
         """x rotated, into `out` (x itself: in place; None: a new dense tensor).
-        positions: int32, (n or 1) x len x axes."""
+        positions: int32, (n or 1) x len x axes. stream: a hipStream_t in place
+        of torch's current stream; needs `out`."""
         try:
             key = (x.shape, x.stride(), x.dtype, positions.shape, positions.stride(), positions.dtype, _sig(out))
             call = self._layouts.get(key)
@@ -232,6 +234,8 @@ class Rotary:
             key = call = None
         if call is None:
             call = self._layouts.keep(key, self._check_apply(x, positions, out))
+        if stream is not None and out is None:
+            raise ValueError("a call on a stream of its own needs out: %s" % _ALLOCATED)
         if not _one_device((x, positions, out)):
             _check_device(x.device, x=x, positions=positions, out=out)
         if out is None:
@@ -257,7 +261,8 @@ class Rotary:
                       norm="rms", q_out=None, k_out=None, stream=None):
         """The norm ("rms" or "layer") of every head of q and k, times the fp32
         weights (None: ones), rotated. k_positions None: those of q. Returns
-        (q_out, k_out); pass q and k themselves to work in place."""
+        (q_out, k_out); pass q and k themselves to work in place. stream: as in
+        apply; needs both outputs."""
         if k_positions is None:
             k_positions = q_positions
         try:
@@ -269,6 +274,8 @@ class Rotary:
         if call is None:
             call = self._layouts.keep(key, self._check_qk_norm(q, k, q_positions, k_positions, q_weight, k_weight, eps,
                                                                norm, q_out, k_out))
+        if stream is not None and (q_out is None or k_out is None):
+            raise ValueError("a call on a stream of its own needs q_out and k_out: %s" % _ALLOCATED)
         if not _one_device((q, k, q_positions, k_positions, q_weight, k_weight, q_out, k_out)):
             _check_device(q.device, q=q, k=k, q_positions=q_positions, k_positions=k_positions, q_weight=q_weight,
                           k_weight=k_weight, q_out=q_out, k_out=k_out)
@@ -382,8 +389,7 @@ class CrossAttention:
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
         if stream is not None and (out is None or (workspace is None and self.workspace_bytes)):
-            raise ValueError("a call on a stream of its own needs out and workspace: memory allocated here belongs "
-                             "to torch's current stream")
+            raise ValueError("a call on a stream of its own needs out and workspace: %s" % _ALLOCATED)
         if not _one_device((q, k, v, out, key_mask, key_lengths, lse, workspace)):
             _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
                           workspace=workspace)

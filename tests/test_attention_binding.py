@@ -107,3 +107,23 @@ def test_a_workspace_with_gaps_or_repeats_is_refused(fake):
     with pytest.raises(TypeError, match="workspace"):
         plan.forward(q, k, k, workspace=need)
     assert len(plan._lib.calls) == 2
+
+
+def test_rotary_on_a_stream_of_its_own_needs_outputs(fake):
+    """Memory allocated in the call belongs to torch's current stream: a kernel on
+    another stream could write it while freed work of the current one still uses it."""
+    plan, x, pos = isa.Rotary(64), _t(2, 3, 4, 64), _t(2, 3, 1, dtype=torch.int32)
+    plan._lib = Recorder()
+    with pytest.raises(ValueError, match="stream"):
+        plan.apply(x, pos, stream=5)
+    for outs in ({}, {"q_out": x}, {"k_out": x}):
+        with pytest.raises(ValueError, match="stream"):
+            plan.apply_qk_norm(x, _t(2, 3, 4, 64), pos, stream=5, **outs)
+    assert not plan._lib.calls
+    plan.apply(x, pos, out=x, stream=5)
+    y = _t(2, 3, 4, 64)
+    plan.apply_qk_norm(x, y, pos, q_out=x, k_out=y, stream=5)
+    assert [args[-1] for _, args in plan._lib.calls] == [5, 5]
+    plan.apply(x, pos)
+    plan.apply_qk_norm(x, y, pos)
+    assert [args[-1] for _, args in plan._lib.calls[2:]] == [1000, 1000]
