@@ -159,15 +159,21 @@ def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
-def _stream(t, stream):
-    """torch's current stream of t's device as a number. The raw form is asked
-    for directly: building a Stream object costs a microsecond, a quarter of a
-    small call."""
-    if stream is not None:
-        return stream
+def _launch(t, stream, function, *args):
+    """function(*args, stream) with t's device current, since a launch goes to the
+    current device and the default stream of every device is handle 0. stream
+    None: torch's current stream of that device. The raw forms are asked for
+    directly: building a Stream object costs a microsecond, a quarter of a small
+    call."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
+    index = t.get_device()
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    if getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)() == index:
+        return function(*args, stream or None)
+    with torch.cuda.device(index):
+        return function(*args, stream or None)
 
 
 def _one_device(tensors):
@@ -241,8 +247,8 @@ class Rotary:
         if out is None:
             out = self._torch.empty(x.shape, dtype=x.dtype, device=x.device)
         code, xt, pb, yt = call
-        st = self._lib.rotary_forward(self.handle, code, xt, x.data_ptr(), positions.data_ptr() or None, pb, yt,
-                                      out.data_ptr(), _stream(x, stream) or None)
+        st = _launch(x, stream, self._lib.rotary_forward, self.handle, code, xt, x.data_ptr(),
+                     positions.data_ptr() or None, pb, yt, out.data_ptr())
         if st:
             _abi.check(st, "rotary_forward")
         return out
@@ -283,10 +289,9 @@ class Rotary:
             q_out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k_out is None:
             k_out = self._torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        st = self._lib.qk_norm_rotary_forward(self.handle, call, q.data_ptr() or None, k.data_ptr() or None,
-                                              _ptr(q_weight), _ptr(k_weight), q_positions.data_ptr() or None,
-                                              k_positions.data_ptr() or None, q_out.data_ptr() or None,
-                                              k_out.data_ptr() or None, _stream(q, stream) or None)
+        st = _launch(q, stream, self._lib.qk_norm_rotary_forward, self.handle, call, q.data_ptr() or None,
+                     k.data_ptr() or None, _ptr(q_weight), _ptr(k_weight), q_positions.data_ptr() or None,
+                     k_positions.data_ptr() or None, q_out.data_ptr() or None, k_out.data_ptr() or None)
         if st:
             _abi.check(st, "qk_norm_rotary_forward")
         return q_out, k_out
@@ -397,11 +402,10 @@ class CrossAttention:
             out = self._torch.empty_strided(*self._like[3], dtype=self.dtype, device=q.device)
         if workspace is None and self.workspace_bytes:
             workspace = self.new_workspace(q.device)
-        st = self._lib.cross_attention_forward(self.handle, q.data_ptr() or None, k.data_ptr() or None,
-                                               v.data_ptr() or None, _ptr(key_mask), _ptr(key_lengths),
-                                               out.data_ptr() or None, _ptr(lse), _ptr(workspace),
-                                               workspace.numel() * workspace.element_size()
-                                               if workspace is not None else 0, _stream(q, stream) or None)
+        st = _launch(q, stream, self._lib.cross_attention_forward, self.handle, q.data_ptr() or None,
+                     k.data_ptr() or None, v.data_ptr() or None, _ptr(key_mask), _ptr(key_lengths),
+                     out.data_ptr() or None, _ptr(lse), _ptr(workspace),
+                     workspace.numel() * workspace.element_size() if workspace is not None else 0)
         if st:
             _abi.check(st, "cross_attention_forward")
         return out

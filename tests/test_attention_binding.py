@@ -127,3 +127,37 @@ def test_rotary_on_a_stream_of_its_own_needs_outputs(fake):
     plan.apply(x, pos)
     plan.apply_qk_norm(x, y, pos)
     assert [args[-1] for _, args in plan._lib.calls[2:]] == [1000, 1000]
+
+
+def test_calls_make_the_device_of_their_tensors_current(fake):
+    """A launch goes to the current device, and torch's default stream is handle 0
+    on every one: without the switch the kernel would run on another GPU."""
+    at = []
+    lib = Recorder(lambda name, args: at.append((name, fake["current"], args[-1])))
+    r, x, pos = isa.Rotary(64), _t(2, 3, 4, 64, index=1), _t(2, 3, 1, dtype=torch.int32, index=1)
+    c = isa.CrossAttention(x, x, x)
+    r._lib = c._lib = lib
+    r.apply(x, pos)
+    r.apply_qk_norm(x, x, pos)
+    c.forward(x, x, x)
+    names = ["rotary_forward", "qk_norm_rotary_forward", "cross_attention_forward"]
+    assert at == [(n, 1, 1001) for n in names]
+    assert fake["current"] == 0
+    # a stream of the caller's belongs to the tensors' device as well
+    at.clear()
+    r.apply(x, pos, out=x, stream=7)
+    assert at == [("rotary_forward", 1, 7)] and fake["current"] == 0
+    # and the device stays where it is for tensors of the current one
+    at.clear()
+    x, pos = _t(2, 3, 4, 64), _t(2, 3, 1, dtype=torch.int32)
+    r.apply(x, pos)
+    r.apply_qk_norm(x, x, pos)
+    c.forward(x, x, x)
+    assert at == [(n, 0, 1000) for n in names]
+
+    def fails(name, args):
+        raise RuntimeError(name)
+    r._lib = Recorder(fails)
+    with pytest.raises(RuntimeError):
+        r.apply(_t(2, 3, 4, 64, index=1), _t(2, 3, 1, dtype=torch.int32, index=1))
+    assert fake["current"] == 0
