@@ -349,8 +349,9 @@ class CrossAttention:
             _check_tokens(out, "out", q.dtype, q.shape[3])
             if out.shape != q.shape:
                 raise ValueError("out has shape %s, q %s" % (tuple(out.shape), tuple(q.shape)))
-        if scale is not None and scale == 0:
-            raise ValueError("scale must not be 0")
+        # Held in fp32, where 0 stands for 1 / sqrt(d).
+        if scale is not None and ctypes.c_float(scale).value == 0.0:
+            raise ValueError("scale must not be 0 in float32, got %r" % (scale,))
         n, lq, hq, d = q.shape
         lk, hkv = k.shape[1], k.shape[2]
         dense = (lq * hq * d, hq * d, d, 1)

@@ -161,3 +161,18 @@ def test_calls_make_the_device_of_their_tensors_current(fake):
     with pytest.raises(RuntimeError):
         r.apply(_t(2, 3, 4, 64, index=1), _t(2, 3, 1, dtype=torch.int32, index=1))
     assert fake["current"] == 0
+
+
+@pytest.mark.parametrize("scale", [1e-46, -1e-60, 1e39, float("nan"), float("inf")])
+def test_a_factor_outside_the_range_of_fp32_is_refused(scale):
+    """The factor is held in fp32, where a smaller one would become 0, which stands
+    for 1 / sqrt(d)."""
+    q, k = torch.zeros(2, 5, 4, 64, dtype=torch.float16), torch.zeros(2, 7, 4, 64, dtype=torch.float16)
+    with pytest.raises((ValueError, isa.ImgStencilError)):
+        isa.CrossAttention(q, k, k, scale=scale)
+
+
+@pytest.mark.parametrize("scale", [1e-44, -1e-30, 2.3e38, -0.125])
+def test_a_factor_of_fp32_is_kept(scale):
+    q, k = torch.zeros(2, 5, 4, 64, dtype=torch.float16), torch.zeros(2, 7, 4, 64, dtype=torch.float16)
+    assert isa.CrossAttention(q, k, k, scale=scale)._desc.scale == torch.tensor(scale, dtype=torch.float32).item()
