@@ -167,7 +167,7 @@ is_status check_attention(const cross_attention_desc *d) {
   if (!d) return IS_ERR_INVALID_ARG;
   if (d->n < 0 || d->lq < 0 || d->lk < 0 || d->hq < 1 || d->hkv < 1 || d->hq % d->hkv || d->d < 1)
     return IS_ERR_INVALID_ARG;
-  if (!isfinite(d->scale) || d->mask_batch_stride < 0) return IS_ERR_INVALID_ARG;
+  if (!isfinite(is::score_factor(d->scale)) || d->mask_batch_stride < 0) return IS_ERR_INVALID_ARG;
   if ((d->dtype != IS_F16 && d->dtype != IS_BF16) || d->d % 8 || d->d > IS_MAX_HEAD_DIM) return IS_ERR_UNSUPPORTED;
   const is_tokens t[4] = {tokens(d->n, d->lq, d->hq, d->q_stride), tokens(d->n, d->lk, d->hkv, d->k_stride),
                           tokens(d->n, d->lk, d->hkv, d->v_stride), tokens(d->n, d->lq, d->hq, d->out_stride)};

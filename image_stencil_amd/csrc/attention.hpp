@@ -3,6 +3,8 @@
 // attention) behind the C ABI.
 #pragma once
 
+#include <math.h>
+
 #include "imgstencil.h"
 
 namespace is {
@@ -53,6 +55,8 @@ struct AttentionPlan {
   int64_t workgroups;     // of one split: n * hkv * runs of row tiles
 };
 
+// What the kernel multiplies scores by: |scale| in units of a power of two.
+inline float score_factor(float scale) { return (float)(fabs((double)scale) * 1.4426950408889634); }
 // Fills everything after d and scale; false when the grid would be too large.
 bool configure_attention(AttentionPlan &p);
 size_t attention_workspace(const AttentionPlan &p);

@@ -1070,7 +1070,7 @@ hipError_t launch_attention(const AttentionPlan &p, const void *q, const void *k
   a.by_splits = divisor((unsigned)p.splits);
   a.by_hkv = divisor((unsigned)d.hkv);
   a.flip = p.scale < 0.f ? 0x80008000u : 0u;
-  a.c = (float)(fabs((double)p.scale) * 1.4426950408889634);
+  a.c = score_factor(p.scale);
   return d.dtype == IS_F16 ? launch_t<_Float16>(p, a, s) : launch_t<__bf16>(p, a, s);
 }
 

@@ -423,7 +423,7 @@ is_status qk_norm_rotary_forward(rotary_plan plan, const qk_norm_desc *d, const 
  *  n, lq, lk, hq, hkv, d: sizes; n, lq and lk may be 0; hq % hkv == 0; d a
  *               multiple of 8, 8 .. IS_MAX_HEAD_DIM
  *  dtype      : IS_F16 or IS_BF16 (q, k, v and out)
- *  scale      : the score factor, finite; 0 stands for 1 / sqrt(d)
+ *  scale      : the score factor; scale * log2(e) finite; 0 stands for 1 / sqrt(d)
  *  q, k, v, out strides: batch, token, head in elements, multiples of 8
  *               (IS_ERR_MISALIGNED), token strides of k and v at most 2^23
  * The scores' products are fp32 sums of 16-bit products; the softmax is fp32;
