@@ -154,7 +154,7 @@ is_status run_rotary(const is::RotaryPlan &p, is_dtype dtype, int norm, float ep
   const int vec = is::rotary_vector_width(p, dtype);
   double blocks = 0.0;
   for (int i = 0; i < nparts; ++i) blocks += (double)is::rotary_blocks(p, vec, parts[i].xt);
-  if (blocks > 2147483647.0) return IS_ERR_UNSUPPORTED;
+  if (blocks * is::kRotaryBlock > is::kMaxThreads) return IS_ERR_UNSUPPORTED;
   if (blocks == 0.0) return IS_OK;
   return is::report_hip(is::launch_rotary(p, dtype, norm, eps, parts, nparts, stream));
 }

@@ -35,7 +35,8 @@ hipError_t launch_rotary(const RotaryPlan &p, is_dtype dtype, int norm, float ep
 // Elements a lane of the rotary kernel moves per access: 16 bytes, 8 or one
 // element (host only; the launcher's rule).
 int rotary_vector_width(const RotaryPlan &p, is_dtype dtype);
-// Blocks of 256 threads that one part takes (host only; the launcher's rule).
+// Blocks of kRotaryBlock threads that one part takes (host only; the launcher's rule).
+constexpr int kRotaryBlock = 256;
 int64_t rotary_blocks(const RotaryPlan &p, int vec, const is_tokens &t);
 
 struct AttentionPlan {
@@ -55,8 +56,12 @@ struct AttentionPlan {
   int64_t workgroups;     // of one split: n * hkv * runs of row tiles
 };
 
+// A launch counts its threads in 32 bits.
+constexpr double kMaxThreads = 4294967295.0;
+
 // What the kernel multiplies scores by: |scale| in units of a power of two.
 inline float score_factor(float scale) { return (float)(fabs((double)scale) * 1.4426950408889634); }
+
 // Fills everything after d and scale; false when the grid would be too large.
 bool configure_attention(AttentionPlan &p);
 size_t attention_workspace(const AttentionPlan &p);

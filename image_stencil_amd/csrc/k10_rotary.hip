@@ -34,7 +34,7 @@
 namespace is {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRotaryBlock;
 constexpr int kHeadsAhead = 4;   // heads a thread loads before it computes
 
 struct Part {

@@ -913,6 +913,14 @@ hipError_t for_head(int dp, F &&f) {
 constexpr int kResidentHead = 128;   // the largest padded head with a RESIDENT form
 constexpr int few_waves(int dp) { return dp <= 128 ? 4 : 2; }
 
+// Threads (log2) that join the splits of 8 elements.
+int join_group(int splits) {
+  int l = 0;
+  while (l < 5 && (1 << l) < splits) ++l;
+  return l;
+}
+int64_t join_items(const AttentionPlan &p) { return (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8); }
+
 template <typename T>
 hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
   const unsigned blocks = (unsigned)((int64_t)a.groups * a.runs);
@@ -931,9 +939,8 @@ hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
     return go(four{}, std::true_type{}, std::false_type{});
   });
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t items = (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8);
-  int log_sg = 0;
-  while (log_sg < 5 && (1 << log_sg) < p.splits) ++log_sg;
+  const int64_t items = join_items(p);
+  const int log_sg = join_group(p.splits);
   return launch_kernel(is_k11_attention_join<T>, dim3((unsigned)(((items << log_sg) + 255) / 256)), dim3(256), 0, s, a,
                        p.tile_rows, log_sg, items);
 }
@@ -996,7 +1003,7 @@ bool configure_attention(AttentionPlan &p) {
   for (int kind = 0; kind < 2; ++kind)
     for (int64_t splits = 1; splits <= 128 && splits * 128 <= d.lk + 127; splits += splits < 16 ? 1 : splits / 8) {
       if (kind == 1 && p.rows <= 32) break;   // a shared tile would leave waves without rows
-      if (splits > 1 && (double)d.n * d.hkv * p.rows * d.d > 2147483647.0) break;   // the joining grid
+      if (splits > 1 && (double)(join_items(p) << join_group((int)splits)) + 255.0 > kMaxThreads) break;
       const Cut c = estimate(p, kind == 0, splits);
       if (c.us < best.us) best = c;
     }
@@ -1024,7 +1031,7 @@ bool configure_attention(AttentionPlan &p) {
     p.lds = few ? Geo<DP, few_waves(DP), false, false>::BYTES : Geo<DP, 4, true, false>::BYTES;
     return hipSuccess;
   });
-  return p.units * p.splits <= 2147483647;
+  return (double)p.workgroups * p.splits * p.block <= kMaxThreads;
 }
 
 size_t attention_workspace(const AttentionPlan &p) {

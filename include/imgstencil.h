@@ -384,7 +384,9 @@ is_status rotary_get_frequencies(rotary_plan plan, double *f, int max, int *coun
  *             pos_batch_stride elements apart (0: one set for the whole batch);
  *             4-byte aligned; any value. May be NULL when rot is 0.
  * y may be x itself with the same strides (in place); otherwise the address
- * ranges must not intersect (IS_ERR_INVALID_ARG). */
+ * ranges must not intersect (IS_ERR_INVALID_ARG). A tensor that
+ * needs 2^32 or more threads (a thread takes at least two elements) is
+ * IS_ERR_UNSUPPORTED. */
 is_status rotary_forward(rotary_plan plan, is_dtype dtype, const is_tokens *xt, const void *x,
                          const int32_t *positions, int64_t pos_batch_stride, const is_tokens *yt, void *y,
                          hipStream_t stream);
@@ -440,7 +442,7 @@ typedef struct cross_attention_plan_s *cross_attention_plan;
 
 /* Check a descriptor and choose a kernel. Host only; immutable, shared by
  * threads and streams. Errors: IS_ERR_INVALID_ARG, IS_ERR_UNSUPPORTED (dtype,
- * d, sizes beyond 2^31 workgroups, strides beyond the limits),
+ * d, sizes that need 2^32 or more threads, strides beyond the limits),
  * IS_ERR_MISALIGNED (strides), IS_ERR_NO_MEMORY. */
 is_status cross_attention_create(const cross_attention_desc *d, cross_attention_plan *out);
 void cross_attention_destroy(cross_attention_plan plan);
