@@ -54,28 +54,54 @@ is_status check_tokens(const is_tokens &t, int d, int es) {
   return IS_OK;
 }
 
+struct Dim {
+  int64_t stride;
+  int size;
+};
+// The dimensions of more than one step, the smallest stride first; returns their number.
+int by_stride(const is_tokens &t, Dim *dims) {
+  const Dim all[3] = {{t.batch_stride, t.n}, {t.token_stride, t.len}, {t.head_stride, t.heads}};
+  int n = 0;
+  for (const Dim &m : all) {
+    if (m.size <= 1) continue;
+    int i = n++;
+    for (; i > 0 && dims[i - 1].stride > m.stride; --i) dims[i] = dims[i - 1];
+    dims[i] = m;
+  }
+  return n;
+}
+
 // An output's elements must have addresses of their own: sorted by stride,
 // every dimension steps over all that the smaller ones span. (A sufficient
 // condition, met by every tensor sliced or permuted from a dense one.)
 bool distinct(const is_tokens &t, int d) {
-  struct Dim {
-    int64_t stride;
-    int size;
-  } dims[3] = {{t.batch_stride, t.n}, {t.token_stride, t.len}, {t.head_stride, t.heads}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (dims[j].stride < dims[i].stride) {
-        const Dim x = dims[i];
-        dims[i] = dims[j];
-        dims[j] = x;
-      }
+  Dim dims[3];
   double span = d;
-  for (const Dim &m : dims) {
-    if (m.size <= 1) continue;
-    if ((double)m.stride < span) return false;
-    span += (double)(m.size - 1) * m.stride;
+  for (int i = 0, n = by_stride(t, dims); i < n; ++i) {
+    if ((double)dims[i].stride < span) return false;
+    span += (double)(dims[i].size - 1) * dims[i].stride;
   }
   return true;
+}
+
+// Every address from the first element to the last belongs to the tensor.
+bool gapless(const is_tokens &t, int d) {
+  Dim dims[3];
+  double span = d;
+  for (int i = 0, n = by_stride(t, dims); i < n; ++i) {
+    if ((double)dims[i].stride > span) return false;
+    span += (double)(dims[i].size - 1) * dims[i].stride;
+  }
+  return true;
+}
+
+// Two tensors certainly share an address: one base, or the base of one among
+// the other's elements where those leave no gap. Slices of a packed buffer, which
+// lie between each other, do not.
+bool collide(const void *p, const is_tokens &tp, const void *q, const is_tokens &tq, int d, int es) {
+  const Range a = range(p, tp, d, es), b = range(q, tq, d, es);
+  if (!intersect(a, b)) return false;
+  return a.lo == b.lo || (a.lo < b.lo ? gapless(tp, d) : gapless(tq, d));
 }
 
 is_status check_rotary(const rotary_desc *d) {
@@ -115,6 +141,19 @@ void frequencies(is::RotaryPlan &p) {
 
 bool dtype_ok(is_dtype t) { return t == IS_F32 || t == IS_F16 || t == IS_BF16; }
 
+// Bytes of a part's position rows, and the range they are read from.
+double positions_bytes(const is::RotaryPlan &p, const is::RotaryPart &a) {
+  return 4.0 * ((double)(a.xt.n - 1) * a.pos_batch_stride + (double)a.xt.len * p.d.axes);
+}
+Range positions_range(const is::RotaryPlan &p, const is::RotaryPart &a) {
+  const char *c = reinterpret_cast<const char *>(a.positions);
+  return {c, p.d.rot > 0 ? c + (size_t)positions_bytes(p, a) : c};
+}
+Range weight_range(const is::RotaryPlan &p, const is::RotaryPart &a) {
+  const char *c = reinterpret_cast<const char *>(a.weight);
+  return {c, c ? c + 4 * (size_t)p.d.d : c};
+}
+
 // One tensor of a rotary call: its checks, before any GPU call.
 is_status check_part(const is::RotaryPlan &p, is_dtype dtype, const is::RotaryPart &a) {
   const int es = element_bytes(dtype), d = p.d.d;
@@ -132,17 +171,20 @@ is_status check_part(const is::RotaryPlan &p, is_dtype dtype, const is::RotaryPa
   const bool in_place = a.x == a.y && a.xt.batch_stride == a.yt.batch_stride &&
                         a.xt.token_stride == a.yt.token_stride && a.xt.head_stride == a.yt.head_stride;
   if (!in_place && intersect(range(a.x, a.xt, d, es), out)) return IS_ERR_INVALID_ARG;
-  if (p.d.rot > 0) {
-    const double words = (double)(a.xt.n - 1) * a.pos_batch_stride + (double)a.xt.len * p.d.axes;
-    if (words * 4.0 > kMaxBytes) return IS_ERR_UNSUPPORTED;
-    const char *c = reinterpret_cast<const char *>(a.positions);
-    if (intersect({c, c + (size_t)(words * 4.0)}, out)) return IS_ERR_INVALID_ARG;
-  }
-  if (a.weight) {
-    const char *c = reinterpret_cast<const char *>(a.weight);
-    if (intersect({c, c + 4 * (size_t)d}, out)) return IS_ERR_INVALID_ARG;
-  }
+  if (p.d.rot > 0 && positions_bytes(p, a) > kMaxBytes) return IS_ERR_UNSUPPORTED;
+  const Range pos = positions_range(p, a), weight = weight_range(p, a);
+  if (intersect(pos, out) || intersect(weight, out)) return IS_ERR_INVALID_ARG;
   return IS_OK;
+}
+
+// What one part writes must not be what the other reads or writes: they run in one
+// launch, in no order.
+bool apart(const is::RotaryPlan &p, is_dtype dtype, const is::RotaryPart &a, const is::RotaryPart &b) {
+  if (empty(a.xt) || empty(b.xt)) return true;
+  const int es = element_bytes(dtype), d = p.d.d;
+  const Range out = range(a.y, a.yt, d, es);
+  return !collide(a.y, a.yt, b.x, b.xt, d, es) && !collide(a.y, a.yt, b.y, b.yt, d, es) &&
+         !intersect(out, positions_range(p, b)) && !intersect(out, weight_range(p, b));
 }
 
 is_status run_rotary(const is::RotaryPlan &p, is_dtype dtype, int norm, float eps, const is::RotaryPart *parts,
@@ -151,6 +193,8 @@ is_status run_rotary(const is::RotaryPlan &p, is_dtype dtype, int norm, float ep
     const is_status st = check_part(p, dtype, parts[i]);
     if (st != IS_OK) return st;
   }
+  if (nparts == 2 && !(apart(p, dtype, parts[0], parts[1]) && apart(p, dtype, parts[1], parts[0])))
+    return IS_ERR_INVALID_ARG;
   const int vec = is::rotary_vector_width(p, dtype);
   double blocks = 0.0;
   for (int i = 0; i < nparts; ++i) blocks += (double)is::rotary_blocks(p, vec, parts[i].xt);
@@ -264,8 +308,6 @@ is_status qk_norm_rotary_forward(rotary_plan plan, const qk_norm_desc *d, const 
     return IS_ERR_INVALID_ARG;
   const is::RotaryPart parts[2] = {{q, q_out, q_weight, q_positions, d->q_pos_batch_stride, d->q, d->q_out},
                                    {k, k_out, k_weight, k_positions, d->k_pos_batch_stride, d->k, d->k_out}};
-  // The two outputs may interleave in one packed buffer, but not start at one address.
-  if (q_out && q_out == k_out && !empty(d->q) && !empty(d->k)) return IS_ERR_INVALID_ARG;
   return run_rotary(plan->p, d->dtype, d->norm, d->eps, parts, 2, stream);
 }
 

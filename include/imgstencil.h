@@ -399,8 +399,11 @@ is_status rotary_forward(rotary_plan plan, is_dtype dtype, const is_tokens *xt, 
  *  IS_NORM_LAYER: norm(x) = (x - mean) / sqrt(mean((x - mean)^2) + eps)
  * Weights are d fp32 values (16-byte aligned) or NULL for ones; eps >= 0,
  * finite. Position arguments, dtypes and the in-place rule as in
- * rotary_forward, for (q, q_out) and (k, k_out); the outputs must not touch
- * the other input's elements. Either tensor may be empty. */
+ * rotary_forward, for (q, q_out) and (k, k_out); an output must not touch
+ * what belongs to the other tensor: its elements, output, weights or positions
+ * (IS_ERR_INVALID_ARG, except where tensors with gaps meet between each other's
+ * elements, as slices of one packed projection do without harm: there it is the
+ * caller's to keep them apart). Either tensor may be empty. */
 typedef enum { IS_NORM_RMS = 1, IS_NORM_LAYER = 2 } is_norm;
 
 typedef struct {

@@ -60,3 +60,44 @@ def test_rotary_calls_fit_a_launch():
         d = _abi.qk_norm_desc(_abi.IS_F16, _abi.IS_NORM_RMS, 1e-6, _tokens(), t, _tokens(), t, 0, 0)
         assert lib.qk_norm_rotary_forward(plan.handle, ctypes.byref(d), A, far, None, None, POS, 3 * far, B, 2 * far,
                                           None) == UNSUPPORTED
+
+
+def test_qk_norm_refuses_outputs_over_the_other_tensor():
+    """Queries and keys run in one launch, in no order: what one of them writes must
+    not be what the other still reads (its elements, weights or positions) or
+    writes."""
+    lib, plan = _abi.load(), isa.Rotary(64)
+    Q, K, QO, KO = 0x100000, 0x400000, 0x900000, 0xC00000
+    WQ, WK, PQ, PK = 0x1000, 0x2000, 0xE00000, 0xF00000
+
+    def st(q=Q, k=K, wq=WQ, wk=WK, qo=QO, ko=KO, qp=PQ, kp=PK, tokens=None):
+        tq, tk, tqo, tko = tokens or (_tokens(), _tokens(heads=2), _tokens(), _tokens(heads=2))
+        d = _abi.qk_norm_desc(_abi.IS_BF16, _abi.IS_NORM_RMS, 1e-6, tq, tk, tqo, tko, 0, 0)
+        return lib.qk_norm_rotary_forward(plan.handle, ctypes.byref(d), q, k, wq, wk, qp, kp, qo, ko, None)
+
+    assert st(qo=K) == INVALID and st(ko=Q) == INVALID and st(qo=K, ko=Q) == INVALID
+    assert st(qo=K + 64) == INVALID and st(ko=Q + 64) == INVALID      # dense tensors over each other
+    assert st(qo=K - 64) == INVALID and st(ko=QO + 128) == INVALID
+    assert st(qo=WK - 32) == INVALID and st(ko=WQ - 32) == INVALID    # weights
+    assert st(qo=PK - 16) == INVALID and st(ko=PQ - 16) == INVALID    # positions
+    # a wide q_out whose row holds the start of a dense k
+    wide = _tokens(token_stride=4 * 64 * 3, batch_stride=3 * 4 * 64 * 3)
+    assert st(qo=K, tokens=(_tokens(), _tokens(heads=2), wide, _tokens(heads=2))) == INVALID
+    # Slices of one packed projection, in place or into another one, lie between
+    # each other: such a call gets past these checks, to the one for its size.
+    far, n4 = 1 << 44, 4 * 64
+    for token, batch, k_at in ((8 * 64, 0, n4 * 2),                          # heads of a token together
+                               (64, 8 * 64 * 2 ** 30, n4 * 2 ** 30 * 2),     # tokens of a head together
+                               (16 * 64, 0, 64 * 2)):                        # heads of q and k in turn
+        head = {64: 64 * 2 ** 30}.get(token, 64 if token == 8 * 64 else 128)
+        t4, t2 = (_tokens(n=1, length=2 ** 30, heads=h, token_stride=token, head_stride=head, batch_stride=batch)
+                  for h in (4, 2))
+        huge = (t4, t2, t4, t2)
+        at = 1 << 40
+        assert st(q=at, k=at + k_at, qo=at, ko=at + k_at, tokens=huge) == UNSUPPORTED, token
+        assert st(q=at, k=at + k_at, qo=far, ko=far + k_at, tokens=huge) == UNSUPPORTED, token
+        assert st(q=at, k=at + k_at, qo=at + k_at, ko=far, tokens=huge) == INVALID, token
+    # a tensor without elements overlaps nothing
+    none = _tokens(length=0)
+    t = _tokens(n=1, length=2 ** 30)
+    assert st(q=1 << 40, qo=1 << 40, k=1 << 40, ko=1 << 40, tokens=(t, none, t, none)) == UNSUPPORTED
