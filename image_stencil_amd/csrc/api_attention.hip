@@ -84,6 +84,12 @@ bool distinct(const is_tokens &t, int d) {
   return true;
 }
 
+// Of two tensors of one size; the stride of a single step says nothing.
+bool same_strides(const is_tokens &a, const is_tokens &b) {
+  return (a.n <= 1 || a.batch_stride == b.batch_stride) && (a.len <= 1 || a.token_stride == b.token_stride) &&
+         (a.heads <= 1 || a.head_stride == b.head_stride);
+}
+
 // Every address from the first element to the last belongs to the tensor.
 bool gapless(const is_tokens &t, int d) {
   Dim dims[3];
@@ -168,8 +174,7 @@ is_status check_part(const is::RotaryPlan &p, is_dtype dtype, const is::RotaryPa
   if (misaligned(a.x, 16) || misaligned(a.y, 16) || misaligned(a.positions, 4) || misaligned(a.weight, 16))
     return IS_ERR_MISALIGNED;
   const Range out = range(a.y, a.yt, d, es);
-  const bool in_place = a.x == a.y && a.xt.batch_stride == a.yt.batch_stride &&
-                        a.xt.token_stride == a.yt.token_stride && a.xt.head_stride == a.yt.head_stride;
+  const bool in_place = a.x == a.y && same_strides(a.xt, a.yt);
   if (!in_place && intersect(range(a.x, a.xt, d, es), out)) return IS_ERR_INVALID_ARG;
   if (p.d.rot > 0 && positions_bytes(p, a) > kMaxBytes) return IS_ERR_UNSUPPORTED;
   const Range pos = positions_range(p, a), weight = weight_range(p, a);

@@ -101,3 +101,16 @@ def test_qk_norm_refuses_outputs_over_the_other_tensor():
     none = _tokens(length=0)
     t = _tokens(n=1, length=2 ** 30)
     assert st(q=1 << 40, qo=1 << 40, k=1 << 40, ko=1 << 40, tokens=(t, none, t, none)) == UNSUPPORTED
+
+
+def test_strides_of_single_steps_do_not_matter_in_place():
+    """The stride of a dimension of one element says nothing: x and y at one base
+    that differ only there are the same tensor (the call gets to the check of its
+    size)."""
+    lib, plan = _abi.load(), isa.Rotary(64)
+    x = _tokens(n=1, length=2 ** 30, heads=1)
+    for kw in ({"batch_stride": 5}, {"head_stride": 1 << 40}, {"batch_stride": 0, "head_stride": 0}):
+        y = _tokens(n=1, length=2 ** 30, heads=1, **kw)
+        assert lib.rotary_forward(plan.handle, _abi.IS_F16, x, 1 << 40, POS, 0, y, 1 << 40, None) == UNSUPPORTED, kw
+    y = _tokens(n=1, length=2 ** 30, heads=1, token_stride=128)
+    assert lib.rotary_forward(plan.handle, _abi.IS_F16, x, 1 << 40, POS, 0, y, 1 << 40, None) == INVALID
