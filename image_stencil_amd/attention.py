@@ -334,6 +334,12 @@ def _check_qkv(q, k, v):
         raise ValueError("%d query heads do not share %d key heads evenly" % (q.shape[2], k.shape[2]))
 
 
+def _steps(shape, stride):
+    """The strides that lead from one element to another: not those of dimensions
+    of one element, and none of an empty tensor's."""
+    return None if 0 in shape else tuple(s if n > 1 else 0 for n, s in zip(shape, stride))
+
+
 class CrossAttention:
     """The plan of cross attention for tensors laid out like q (n x lq x hq x d),
     k and v (n x lk x hkv x d) and out (like q; None: dense). Only shapes,
@@ -418,7 +424,7 @@ class CrossAttention:
                 continue
             if not isinstance(t, torch.Tensor) or t.dtype != self.dtype:
                 raise TypeError("%s must be a %s tensor" % (name, self.dtype))
-            if t.shape != shape or t.stride() != stride:
+            if t.shape != shape or _steps(shape, t.stride()) != _steps(shape, stride):
                 raise ValueError("%s is %s with strides %s, the plan is for %s with strides %s"
                                  % (name, tuple(t.shape), t.stride(), shape, stride))
         n, lq, hq, lk = self._desc.n, self._desc.lq, self._desc.hq, self._desc.lk

@@ -176,3 +176,23 @@ def test_a_factor_outside_the_range_of_fp32_is_refused(scale):
 def test_a_factor_of_fp32_is_kept(scale):
     q, k = torch.zeros(2, 5, 4, 64, dtype=torch.float16), torch.zeros(2, 7, 4, 64, dtype=torch.float16)
     assert isa.CrossAttention(q, k, k, scale=scale)._desc.scale == torch.tensor(scale, dtype=torch.float32).item()
+
+
+def test_a_plan_serves_tensors_that_differ_in_strides_of_single_steps(fake):
+    """The stride of a dimension of one element says nothing: a batch of one sliced
+    out of a wider tensor, or a single token of a cache, lies as the plan expects."""
+    q, k = _t(1, 5, 4, 64), _t(1, 1, 4, 64)
+    plan = isa.CrossAttention(q, k, k, q)
+    plan._lib = Recorder()
+    q2 = gpu(torch.zeros(3, 5, 4, 64, dtype=torch.float16)[:, :, :][1:2].as_strided((1, 5, 4, 64), (7, 256, 64, 1)))
+    k2 = gpu(torch.zeros(1, 9, 4, 64, dtype=torch.float16)[:, 3:4].as_strided((1, 1, 4, 64), (11, 1 << 30, 64, 1)))
+    plan.forward(q2, k2, k2, q2)
+    assert len(plan._lib.calls) == 1
+    for bad in (_t(1, 5, 8, 64)[:, :, :4], _t(1, 4, 5, 64).transpose(1, 2)):
+        with pytest.raises(ValueError, match="the plan is for"):
+            plan.forward(bad, k, k, q)
+    empty = _t(1, 0, 4, 64)
+    plan = isa.CrossAttention(q, empty, empty, q)
+    plan._lib = Recorder()
+    plan.forward(q, empty.as_strided((1, 0, 4, 64), (64, 256, 128, 1)), empty, q)
+    assert len(plan._lib.calls) == 1
