@@ -1058,6 +1058,9 @@ hipError_t launch_attention(const AttentionPlan &p, const void *q, const void *k
     a.vs[i] = d.v_stride[i];
     a.os[i] = d.out_stride[i];
   }
+  // One key has no next one: its stride may be anything, and the kernel forms the
+  // span of a whole tile from it in 32 bits.
+  if (d.lk <= 1) a.ks[1] = a.vs[1] = 0;
   a.mask_bs = d.mask_batch_stride;
   a.lq = d.lq;
   a.lk = d.lk;
