@@ -322,9 +322,12 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
     if constexpr (!MASK) return 0;
     return (uint8_t)lds[G::MASKS + wave * G::MASK_WAVE + (j & (G::MASK_SLOTS - 1)) * G::MASK_SLOT + skip + lane % KT];
   };
+  uint64_t visible = 0;   // of all tiles so far
   auto vote = [&](int j, uint8_t byte) -> uint64_t {
     if constexpr (!MASK) return 0;
-    return __ballot(lane < KT && tile_key(j) + lane < keys && byte != 0);
+    const uint64_t bits = __ballot(lane < KT && tile_key(j) + lane < keys && byte != 0);
+    visible |= bits;
+    return bits;
   };
   auto seen = [&](int j) -> uint64_t { return vote(j, mask_byte(j)); };
 
@@ -726,6 +729,22 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
          none);
     // The tiles past the last: LDS is used again below, and by the next workgroup.
     if constexpr (!SHARED) arrived(std::integral_constant<int, 0>{});
+  }
+
+  // No key was seen: nothing is added, whatever q holds. (An infinite q times the
+  // zeros in place of a row that was not fetched is NaN, and its p with it.)
+  if constexpr (MASK) {
+    if (visible == 0) {
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb) {
+        m[qb] = -FLT_MAX;
+        l[qb] = 0.f;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[qb][mb][e] = 0.f;
+      }
+    }
   }
 
   // ---- Results: lane = row n32, elements 32 mb + 8 a + 4 half + (0..3) of o.
