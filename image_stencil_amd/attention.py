@@ -159,21 +159,14 @@ def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
-def _launch(t, stream, function, *args):
-    """function(*args, stream) with t's device current, since a launch goes to the
-    current device and the default stream of every device is handle 0. stream
-    None: torch's current stream of that device. The raw forms are asked for
-    directly: building a Stream object costs a microsecond, a quarter of a small
-    call."""
+def _device_calls():
+    """(the current device's index, the current stream of a device as a number).
+    torch's raw forms, bound once per plan: building a Stream object costs a
+    microsecond, a quarter of a small call."""
     import torch
-    index = t.get_device()
-    if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
-    if getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)() == index:
-        return function(*args, stream or None)
-    with torch.cuda.device(index):
-        return function(*args, stream or None)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+            raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _one_device(tensors):
@@ -220,6 +213,7 @@ class Rotary:
                            ramp[0], ramp[1], magnitude)
         self.handle = rotary_create(desc)
         self._lib, self._layouts = _abi.load(), _Layouts()
+        self._current_device, self._current_stream = _device_calls()
         # Bound now: at interpreter exit the module's globals may already be
         # gone when __del__ runs.
         self._destroy = self._lib.rotary_destroy
@@ -244,11 +238,17 @@ class Rotary:
             raise ValueError("a call on a stream of its own needs out: %s" % _ALLOCATED)
         if not _one_device((x, positions, out)):
             _check_device(x.device, x=x, positions=positions, out=out)
+        index = x.get_device()
+        if self._current_device() != index:     # a launch goes to the current device
+            with self._torch.cuda.device(index):
+                return self.apply(x, positions, out, stream)
         if out is None:
             out = self._torch.empty(x.shape, dtype=x.dtype, device=x.device)
         code, xt, pb, yt = call
-        st = _launch(x, stream, self._lib.rotary_forward, self.handle, code, xt, x.data_ptr(),
-                     positions.data_ptr() or None, pb, yt, out.data_ptr())
+        if stream is None:
+            stream = self._current_stream(index)
+        st = self._lib.rotary_forward(self.handle, code, xt, x.data_ptr(), positions.data_ptr() or None, pb, yt,
+                                      out.data_ptr(), stream or None)
         if st:
             _abi.check(st, "rotary_forward")
         return out
@@ -285,13 +285,21 @@ class Rotary:
         if not _one_device((q, k, q_positions, k_positions, q_weight, k_weight, q_out, k_out)):
             _check_device(q.device, q=q, k=k, q_positions=q_positions, k_positions=k_positions, q_weight=q_weight,
                           k_weight=k_weight, q_out=q_out, k_out=k_out)
+        index = q.get_device()
+        if self._current_device() != index:     # a launch goes to the current device
+            with self._torch.cuda.device(index):
+                return self.apply_qk_norm(q, k, q_positions, k_positions, q_weight, k_weight, eps, norm, q_out, k_out,
+                                          stream)
         if q_out is None:
             q_out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k_out is None:
             k_out = self._torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        st = _launch(q, stream, self._lib.qk_norm_rotary_forward, self.handle, call, q.data_ptr() or None,
-                     k.data_ptr() or None, _ptr(q_weight), _ptr(k_weight), q_positions.data_ptr() or None,
-                     k_positions.data_ptr() or None, q_out.data_ptr() or None, k_out.data_ptr() or None)
+        if stream is None:
+            stream = self._current_stream(index)
+        st = self._lib.qk_norm_rotary_forward(self.handle, call, q.data_ptr() or None, k.data_ptr() or None,
+                                              _ptr(q_weight), _ptr(k_weight), q_positions.data_ptr() or None,
+                                              k_positions.data_ptr() or None, q_out.data_ptr() or None,
+                                              k_out.data_ptr() or None, stream or None)
         if st:
             _abi.check(st, "qk_norm_rotary_forward")
         return q_out, k_out
@@ -369,6 +377,7 @@ class CrossAttention:
                                           *[S(*st[:3]) for (_, st) in self._like], lk)
         self.handle = cross_attention_create(self._desc)
         self._lib, self._layouts = _abi.load(), _Layouts()
+        self._current_device, self._current_stream = _device_calls()
         self._destroy = self._lib.cross_attention_destroy
         self.workspace_bytes = cross_attention_workspace_size(self.handle)
 
@@ -405,14 +414,21 @@ class CrossAttention:
         if not _one_device((q, k, v, out, key_mask, key_lengths, lse, workspace)):
             _check_device(q.device, q=q, k=k, v=v, out=out, key_mask=key_mask, key_lengths=key_lengths, lse=lse,
                           workspace=workspace)
+        index = q.get_device()
+        if self._current_device() != index:     # a launch goes to the current device
+            with self._torch.cuda.device(index):
+                return self.forward(q, k, v, out, key_mask, key_lengths, lse, workspace, stream)
         if out is None:
             out = self._torch.empty_strided(*self._like[3], dtype=self.dtype, device=q.device)
         if workspace is None and self.workspace_bytes:
             workspace = self.new_workspace(q.device)
-        st = _launch(q, stream, self._lib.cross_attention_forward, self.handle, q.data_ptr() or None,
-                     k.data_ptr() or None, v.data_ptr() or None, _ptr(key_mask), _ptr(key_lengths),
-                     out.data_ptr() or None, _ptr(lse), _ptr(workspace),
-                     workspace.numel() * workspace.element_size() if workspace is not None else 0)
+        if stream is None:
+            stream = self._current_stream(index)
+        st = self._lib.cross_attention_forward(self.handle, q.data_ptr() or None, k.data_ptr() or None,
+                                               v.data_ptr() or None, _ptr(key_mask), _ptr(key_lengths),
+                                               out.data_ptr() or None, _ptr(lse), _ptr(workspace),
+                                               workspace.numel() * workspace.element_size()
+                                               if workspace is not None else 0, stream or None)
         if st:
             _abi.check(st, "cross_attention_forward")
         return out
