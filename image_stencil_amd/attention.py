@@ -16,6 +16,7 @@ _LAYOUTS = {"half": _abi.IS_ROTARY_HALF, "interleaved": _abi.IS_ROTARY_INTERLEAV
 _SCALINGS = {"none": _abi.IS_ROTARY_UNSCALED, "linear": _abi.IS_ROTARY_LINEAR, "ntk": _abi.IS_ROTARY_NTK,
              "ramp": _abi.IS_ROTARY_RAMP}
 _NORMS = {"rms": _abi.IS_NORM_RMS, "layer": _abi.IS_NORM_LAYER}
+_INT_MAX = 2147483647   # the descriptors hold sizes as int
 _ALLOCATED = "memory allocated here belongs to torch's current stream"
 
 
@@ -106,6 +107,8 @@ def _check_tokens(t, name, dtype, d=None):
         raise TypeError("%s must be a %s tensor" % (name, dtype))
     if t.dim() != 4:
         raise ValueError("%s must be n x len x heads x d, got shape %s" % (name, tuple(t.shape)))
+    if max(t.shape) > _INT_MAX:
+        raise ValueError("%s has a dimension over %d, got shape %s" % (name, _INT_MAX, tuple(t.shape)))
     if d is not None and t.shape[3] != d:
         raise ValueError("%s has %d elements per head, expected %d" % (name, t.shape[3], d))
     if t.shape[3] > 1 and t.stride(3) != 1:

@@ -196,3 +196,22 @@ def test_a_plan_serves_tensors_that_differ_in_strides_of_single_steps(fake):
     plan._lib = Recorder()
     plan.forward(q, empty.as_strided((1, 0, 4, 64), (64, 256, 128, 1)), empty, q)
     assert len(plan._lib.calls) == 1
+
+
+def test_sizes_beyond_the_descriptors_are_refused():
+    """The C descriptors hold sizes as int: larger ones would be cut to their low
+    32 bits and a part of the tensor would be left out, without an error."""
+    def meta(*shape, dtype=torch.float16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    r = isa.Rotary(64)
+    for n, length, heads in ((2 ** 32 + 2, 3, 4), (2, 2 ** 32 + 3, 4), (2, 3, 2 ** 32 + 4), (2 ** 31, 1, 1)):
+        x, pos = meta(n, length, heads, 64), meta(n, length, 1, dtype=torch.int32)
+        for call in (lambda: r.apply(x, pos), lambda: r.apply_qk_norm(x, meta(1, 1, 1, 64), pos, pos[:1, :1]),
+                     lambda: r.apply_qk_norm(meta(1, 1, 1, 64), x, pos[:1, :1], pos)):
+            with pytest.raises(ValueError, match="2147483647"):
+                call()
+    big = 2 ** 32 + 1
+    for q, k in ((meta(big, 1, 1, 64), meta(big, 2, 1, 64)), (meta(1, big, 1, 64), meta(1, 2, 1, 64)),
+                 (meta(1, 1, 1, 64), meta(1, big, 1, 64)), (meta(1, 1, big, 64), meta(1, 2, 1, 64))):
+        with pytest.raises(ValueError, match="2147483647"):
+            isa.CrossAttention(q, k, k)
