@@ -311,6 +311,8 @@ class Rotary:
         code = _dtype(q, "q")
         _check_tokens(q, "q", q.dtype, self.d)
         _check_tokens(k, "k", q.dtype, self.d)
+        if eps > 0 and ctypes.c_float(eps).value == 0.0:
+            raise ValueError("eps must not become 0 in float32, got %r" % (eps,))
         if norm not in _NORMS:
             raise ValueError("norm must be one of %s" % sorted(_NORMS))
         qb = _check_positions(q_positions, q, self.axes, "q_positions")

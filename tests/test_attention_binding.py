@@ -215,3 +215,14 @@ def test_sizes_beyond_the_descriptors_are_refused():
                  (meta(1, 1, 1, 64), meta(1, big, 1, 64)), (meta(1, 1, big, 64), meta(1, 2, 1, 64))):
         with pytest.raises(ValueError, match="2147483647"):
             isa.CrossAttention(q, k, k)
+
+
+def test_an_eps_that_fp32_rounds_to_0_is_refused():
+    """eps is held in fp32: a positive one that becomes 0 turns heads of zeros into
+    NaN."""
+    r, x, pos = isa.Rotary(64), torch.zeros(2, 3, 4, 64), torch.zeros(2, 3, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="eps"):
+        r.apply_qk_norm(x, x, pos, eps=1e-50)
+    for eps in (0.0, 1e-44, 1e-6):
+        with pytest.raises(TypeError, match="on a GPU"):   # past the check
+            r.apply_qk_norm(x, x, pos, eps=eps)
