@@ -119,7 +119,7 @@ is_status check_rotary(const rotary_desc *d) {
   if (d->layout != IS_ROTARY_HALF && d->layout != IS_ROTARY_INTERLEAVED) return IS_ERR_INVALID_ARG;
   if (d->scaling < IS_ROTARY_UNSCALED || d->scaling > IS_ROTARY_RAMP) return IS_ERR_INVALID_ARG;
   if (!(d->base > 0.0) || !isfinite(d->base)) return IS_ERR_INVALID_ARG;
-  if (!(d->magnitude > 0.0) || !isfinite(d->magnitude)) return IS_ERR_INVALID_ARG;
+  if (!((float)d->magnitude > 0.f) || !isfinite((float)d->magnitude)) return IS_ERR_INVALID_ARG;   // used in fp32
   if (d->scaling != IS_ROTARY_UNSCALED && (!(d->factor >= 1.0) || !isfinite(d->factor))) return IS_ERR_INVALID_ARG;
   if (d->scaling == IS_ROTARY_NTK && pairs / d->axes == 1) return IS_ERR_UNSUPPORTED;
   if (d->scaling == IS_ROTARY_RAMP &&

@@ -361,7 +361,7 @@ typedef struct {
   double base;             /* > 0, finite */
   double factor;           /* >= 1, finite (ignored when unscaled) */
   double ramp_low, ramp_high;   /* IS_ROTARY_RAMP: turns, 0 <= low < high */
-  double magnitude;        /* > 0, finite; 1 for none */
+  double magnitude;        /* > 0, finite, both also in fp32; 1 for none */
 } rotary_desc;
 
 typedef struct rotary_plan_s *rotary_plan;

@@ -226,3 +226,13 @@ def test_an_eps_that_fp32_rounds_to_0_is_refused():
     for eps in (0.0, 1e-44, 1e-6):
         with pytest.raises(TypeError, match="on a GPU"):   # past the check
             r.apply_qk_norm(x, x, pos, eps=eps)
+
+
+def test_a_magnitude_outside_the_range_of_fp32_is_refused():
+    """The magnitude is used in fp32: one that becomes 0 or infinite there turns
+    all that it multiplies into that, or NaN."""
+    for magnitude in (1e-46, 1e39):
+        with pytest.raises(isa.ImgStencilError):
+            isa.Rotary(64, magnitude=magnitude)
+    isa.Rotary(64, magnitude=1e-30)
+    isa.Rotary(64, magnitude=1e38)
