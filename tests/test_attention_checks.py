@@ -114,3 +114,62 @@ def test_strides_of_single_steps_do_not_matter_in_place():
         assert lib.rotary_forward(plan.handle, _abi.IS_F16, x, 1 << 40, POS, 0, y, 1 << 40, None) == UNSUPPORTED, kw
     y = _tokens(n=1, length=2 ** 30, heads=1, token_stride=128)
     assert lib.rotary_forward(plan.handle, _abi.IS_F16, x, 1 << 40, POS, 0, y, 1 << 40, None) == INVALID
+
+
+# --------------------------------------------------- plans that split their keys
+SPLIT = dict(n=1, lq=1, lk=40000, hq=8, hkv=1, d=128)
+
+
+def _need(plan):
+    need = ctypes.c_size_t()
+    assert _abi.load().cross_attention_workspace_size(plan, ctypes.byref(need)) == 0
+    return need.value
+
+
+@pytest.mark.parametrize("kw", [SPLIT, dict(n=3, lq=2, lk=9001, hq=4, hkv=4, d=64), dict(n=1, lq=3, lk=20011, hq=2, hkv=2, d=256),
+                                dict(n=1, lq=130, lk=9001, hq=1, hkv=1, d=40)])
+def test_split_plans_cover_the_keys_and_their_workspace_the_parts(kw):
+    """Every key lies in one split, no split is empty, and the workspace holds a
+    row of d values and a log-sum for every row of every row tile and split."""
+    st, plan = _create(_desc(**kw))
+    assert st == 0
+    info = _abi.conv2d_plan_info()
+    assert _abi.load().cross_attention_get_plan_info(plan, ctypes.byref(info)) == 0
+    splits, keys, rows = info.grid_y, info.tile_w, info.tile_h
+    own = b"own" in info.kernel
+    assert splits > 1 and keys % (32 if own else 64) == 0 and rows == (32 if own else 128)
+    assert (splits - 1) * keys < kw["lk"] <= splits * keys
+    tiles = -(-kw["lq"] * (kw["hq"] // kw["hkv"]) // rows)
+    assert info.grid_x == kw["n"] * kw["hkv"] * tiles
+    assert _need(plan) == info.grid_x * splits * rows * (kw["d"] + 1) * 4
+    _abi.load().cross_attention_destroy(plan)
+
+
+def test_plans_without_splits_need_no_workspace():
+    for kw in ({}, dict(lq=16384, lk=16384, hq=16, hkv=4, d=128, n=1), dict(n=8, lq=4096, lk=120, hq=8, hkv=8, d=40)):
+        st, plan = _create(_desc(**kw))
+        assert st == 0 and _need(plan) == 0
+        _abi.load().cross_attention_destroy(plan)
+
+
+def test_workspaces_that_do_not_serve_are_refused():
+    lib = _abi.load()
+    st, plan = _create(_desc(**SPLIT))
+    assert st == 0
+    need = _need(plan)
+    Q, K, V, OUT, LSE, MASK, LEN, WS = (i << 28 for i in range(1, 9))
+    assert need < 1 << 28
+
+    def forward(ws=WS, ws_bytes=need, lse=None, mask=None, lengths=None):
+        return lib.cross_attention_forward(plan, Q, K, V, mask, lengths, OUT, lse, ws, ws_bytes, None)
+
+    assert forward(ws=None) == WORKSPACE and forward(ws=None, ws_bytes=0) == WORKSPACE
+    assert forward(ws_bytes=need - 1) == WORKSPACE and forward(ws_bytes=0) == WORKSPACE
+    assert forward(ws=WS + 8) == MISALIGNED and forward(ws=WS + 1) == MISALIGNED
+    for other in (Q, K, V, OUT):
+        assert forward(ws=other) == INVALID and forward(ws=other - need + 16) == INVALID
+    assert forward(ws=OUT + 8 * 128 * 2 - 16) == INVALID               # the output's last bytes
+    assert forward(lse=LSE, ws=LSE + 16) == INVALID and forward(lse=WS + need - 16) == INVALID
+    assert forward(mask=MASK, ws=MASK + 39984) == INVALID and forward(lengths=LEN, ws=LEN) == INVALID
+    assert forward(mask=WS + need - 1) == INVALID and forward(lengths=WS + need - 4) == INVALID
+    lib.cross_attention_destroy(plan)
