@@ -19,7 +19,7 @@ struct cross_attention_plan_s {
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr long double kTwoPi = 6.283185307179586476925286766559L;
 constexpr double kMaxBytes = 7.0e13;       // one tensor's address range, under 2^46
 
 int element_bytes(is_dtype t) { return t == IS_F32 ? 4 : 2; }
@@ -128,20 +128,25 @@ is_status check_rotary(const rotary_desc *d) {
   return IS_OK;
 }
 
+// In 80 bits, and rounded once: in 64 the powers and quotients would be off by up to
+// 9 halves of a last bit, which far positions multiply.
 void frequencies(is::RotaryPlan &p) {
+  typedef long double real;
   const rotary_desc &d = p.d;
   const int per = p.per_axis = d.rot / 2 / d.axes;
-  const double base = d.scaling == IS_ROTARY_NTK && per > 1 ? d.base * pow(d.factor, per / (per - 1.0)) : d.base;
+  const real base = d.scaling == IS_ROTARY_NTK && per > 1 ? d.base * powl(d.factor, (real)per / (per - 1)) : d.base;
   for (int i = 0; i < per; ++i) {
-    double f = pow(base, -(double)i / per);
+    real f = powl(base, -(real)i / per);
     if (d.scaling == IS_ROTARY_LINEAR) f /= d.factor;
     if (d.scaling == IS_ROTARY_RAMP) {
-      double keep = (d.original_len * f / kTwoPi - d.ramp_low) / (d.ramp_high - d.ramp_low);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-      f = f * keep + f / d.factor * (1.0 - keep);
+      real keep = (d.original_len * f / kTwoPi - d.ramp_low) / ((real)d.ramp_high - d.ramp_low);
+      keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+      f = f * keep + f / d.factor * (1 - keep);
     }
-    p.freq[i] = f;
-    for (int axis = 0; axis < d.axes; ++axis) p.turns[axis * per + i] = f / kTwoPi;
+    p.freq[i] = (double)f;
+    // A position is a whole number: whole turns of it never count.
+    const real turns = f / kTwoPi - rintl(f / kTwoPi);
+    for (int axis = 0; axis < d.axes; ++axis) p.turns[axis * per + i] = (double)turns;
   }
 }
 

@@ -11,12 +11,12 @@ namespace is {
 
 // A rotary plan: the descriptor and each frequency of an axis in turns per
 // position (f / 2 pi, 64 bits), so that an angle is reduced to one turn by
-// dropping whole turns, exactly, before it is rounded to 32 bits.
+// dropping whole turns before it is rounded to 32 bits.
 struct RotaryPlan {
   rotary_desc d;
   int per_axis;                          // Pa = rot / 2 / axes
   double freq[IS_MAX_HEAD_DIM / 2];      // radians per position
-  double turns[IS_MAX_HEAD_DIM / 2];     // turns per position, of every pair (axis after axis)
+  double turns[IS_MAX_HEAD_DIM / 2];     // turns per position, less whole ones, of every pair (axis after axis)
 };
 
 // One tensor of a rotary launch.

@@ -24,8 +24,10 @@
 // loads and without branches, so one trip to memory starts a thread's work. A
 // thread's sines serve all the heads it walks over.
 //
-// The angle is formed in turns in 64 bits, the whole turns are dropped there,
-// and only the rest is rounded to 32 bits: error 2^-26 turns at any position.
+// The angle is formed in turns in 64 bits, the whole turns are dropped inside the
+// product (fma), and only the rest is rounded to 32 bits: off by 2^-26 turns and by
+// 2^-53 of the whole angle, what a 64-bit frequency is short of (as much again from
+// 2^27 turns on; 2^-24.7 turns at positions of 2^31).
 // 16-bit results use the hardware sine of an angle in turns, fp32 results the
 // library's sincospi of twice the angle.
 #include "attention.hpp"
@@ -75,8 +77,8 @@ __device__ __forceinline__ float head_sum(float v, int log_lanes) {
 }
 
 template <typename T>
-__device__ __forceinline__ void sine(double turns, float &s, float &c) {
-  const float t = (float)(turns - rint(turns));   // the rest of a turn, in [-1/2, 1/2]
+__device__ __forceinline__ void sine(double pos, double turns, float &s, float &c) {
+  const float t = (float)fma(pos, turns, -rint(pos * turns));   // the rest of a turn, in [-1/2, 1/2]
   if constexpr (sizeof(T) == 4) {
     sincospif(2.f * t, &s, &c);
   } else {
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
         const int pair = j < N ? first[i] + j : mid[i] + j - N;
         const double f = j < N ? f0[j % N] : f1[j % N];
         const int32_t q = pair < a.per_axis ? q0 : pair < 2 * a.per_axis ? q1 : q2;
-        sine<T>((double)q * f, sn[i][j], cs[i][j]);
+        sine<T>((double)q, f, sn[i][j], cs[i][j]);
         sn[i][j] *= a.magnitude;
         cs[i][j] *= a.magnitude;
       }

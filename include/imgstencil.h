@@ -339,8 +339,10 @@ typedef struct {
  *                    often stay, slow ones are squeezed (the by-parts
  *                    interpolation of YaRN, arXiv 2309.00071, section 3.2, whose
  *                    attention temperature is magnitude = 0.1 ln(factor) + 1)
- * Angles are formed in 64 bits, so far positions lose nothing: fp32 outputs are
- * within a few 2^-24 of |x|, 16-bit outputs within their own rounding plus 2^-20. */
+ * Angles are formed in 64 bits: off by 2^-26 turns, and by 2^-53 of the whole
+ * angle, which counts from about 2^27 turns on. fp32 outputs are within a few 2^-24
+ * of |x| (8 at positions of 2^31), 16-bit outputs within their own rounding plus
+ * 2^-20. */
 typedef enum { IS_ROTARY_HALF = 0, IS_ROTARY_INTERLEAVED = 1 } is_rotary_layout;
 typedef enum {
   IS_ROTARY_UNSCALED = 0,
