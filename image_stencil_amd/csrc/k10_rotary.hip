@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void is_k10_rotary(const Args a) {
               e1[i][j] -= mean;
             }
         }
-        const float inv = __builtin_amdgcn_rsqf(sum_own([](float v) { return v * v; }) + a.eps);
+        const float inv = rsqrtf(sum_own([](float v) { return v * v; }) + a.eps);   // also below the normal numbers
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll

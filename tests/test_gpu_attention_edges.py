@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import attention_oracle as ao
 import image_stencil_amd as isa
 from gpu_util import say
 from test_gpu_cross_attention import _compare, _qkv
@@ -208,3 +209,24 @@ def test_rotary_bases_at_every_16_bytes(dtype, d, rot):
     shifted = torch.zeros(x.numel() + 64, dtype=dtype, device="cuda")[1:1 + x.numel()].view(x.shape)
     with pytest.raises(isa.ImgStencilError):
         plan.apply(shifted, pos)
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("size", [1e-15, 1e-19, 1e-20, 1e-21])
+def test_norms_of_small_heads_without_eps(dtype, kind, size):
+    """eps 0 and heads whose mean square is below fp32's normal numbers: what 32 bits
+    hold of it (steps of 2^-149: squares, their sum and mean are off by half a step
+    each) still gives a norm. A head of zeros has none."""
+    d = 64
+    x = (size * torch.randn(1, 5, 3, d, generator=torch.Generator().manual_seed(7))).to(dtype)
+    pos = torch.zeros(1, 5, 1, dtype=torch.int32, device="cuda")
+    y, _ = isa.Rotary(d, 0).apply_qk_norm(x.cuda(), x[:, :, :1].cuda(), pos, eps=0.0, norm=kind)
+    want, scale = ao.norm(x.double(), torch.ones(d).double(), 0.0, kind)
+    centred = x.double() - (x.double().mean(-1, keepdim=True) if kind == "layer" else 0.0)
+    mean = (centred * centred).mean(-1, keepdim=True)
+    steps = 0.5 * 3 * 2.0 ** -150 / mean
+    bound = ao.rounding(want, dtype) + (1 + ao.half(dtype)) * (ao.norm_error(d, kind) + steps) * scale
+    assert ((y.cpu().double() - want).abs() <= bound).all()
+    z, _ = isa.Rotary(d, 0).apply_qk_norm(torch.zeros_like(x).cuda(), x[:, :, :1].cuda(), pos, eps=0.0, norm=kind)
+    assert torch.isnan(z).all()
