@@ -316,8 +316,9 @@ hipError_t launch_t(bool half, const Args &a, unsigned blocks, hipStream_t s) {
 }  // namespace
 
 // 16 bytes where the head's parts are at least that long (half layout) or made
-// of such chunks (interleaved), else 8, else single elements. Alignment and
-// strides do not matter: the memory path takes a vector at any element.
+// of such chunks (interleaved), else 8, else single elements. Where a head starts
+// does not matter (a base is 16-byte aligned, the strides are free): the memory path
+// takes a vector at any element.
 int rotary_vector_width(const RotaryPlan &p, is_dtype dtype) {
   const int pairs = p.d.rot / 2, rest = p.d.d - p.d.rot;
   for (int v = dtype == IS_F32 ? 4 : 8; v >= 4; v /= 2) {

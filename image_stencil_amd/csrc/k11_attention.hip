@@ -28,13 +28,13 @@
 // offset makes the DMA write zeros); their scores start from -infinity, in the
 // accumulator (MASK) or after the product (the last tile's end).
 //
-// What bounds it, measured on one MI355X: heads of 128, 16384 x 16384 tokens, 16
-// query and 4 key heads, bf16: 1868 us, 1.17 PFLOP/s, the rate of a large library
-// product on the same card, at the clock the power limit leaves. Heads of 64,
-// 3600 x 3600, 16 heads, fp16: 74 us, 0.71 PFLOP/s: per 32 x 32 scores the vector
-// unit's 16 exponentials (8 cycles each), multiply-adds, sums, conversions and
-// maxima take about 230 cycles of a wave and the products 256, and one wave's
-// instructions leave it no faster than one in five cycles. One token over
+// What bounds it, measured on MI355Xs: heads of 128, 16384 x 16384 tokens, 16 query
+// and 4 key heads, bf16: 1868 to 1977 us on different cards, 1.11 to 1.18 PFLOP/s, the
+// rate of a large library product, at the clock the power limit leaves. Heads of
+// 64, 3600 x 3600, 16 heads, fp16: 74 to 78 us, 0.68 to 0.72 PFLOP/s: per 32 x 32 scores
+// the vector unit is active for about 430 cycles (91 instructions: 16 exponentials
+// of 8 cycles each, multiply-adds, sums, conversions and maxima) and the matrix cores
+// for 256, and the two hardly overlap (48% and 28% of the time). One token over
 // 4 x 32771 keys, 2 heads of 128: 30.9 us, 4.3 TB/s of k and v with the join.
 #include <float.h>
 #include <math.h>
@@ -1045,7 +1045,7 @@ bool configure_attention(AttentionPlan &p) {
   }
   p.name = few ? "is_k11_attention (own tiles)" : p.run > 1 ? "is_k11_attention (resident)" : "is_k11_attention";
   p.workgroups = (int64_t)d.n * d.hkv * ((p.row_tiles + p.run - 1) / p.run);
-  for_head(p.dp, [&](auto dp) {
+  (void)for_head(p.dp, [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
     p.lds = few ? Geo<DP, few_waves(DP), false, false>::BYTES : Geo<DP, 4, true, false>::BYTES;
     return hipSuccess;
