@@ -10,7 +10,9 @@ the C ABI of include/imgstencil.h and nothing else. conv2d() and conv_chain()
 are conveniences on torch tensors: torch only allocates device memory and
 supplies the current HIP stream. The attention operators (Rotary,
 CrossAttention, rotary(), qk_norm_rotary(), cross_attention() and their C names)
-are in attention.py.
+are in attention.py, the operators around them (BlockNorm, Dense, block_norm(),
+dense()) in blocks.py, and attention to states held in 8 bits (HeldStates,
+HeldAttention, held_attention()) in held.py.
 """
 import ctypes
 
@@ -21,6 +23,11 @@ from .attention import (CrossAttention, Rotary, cross_attention, cross_attention
                         cross_attention_forward, cross_attention_get_plan_info, cross_attention_workspace_size,
                         qk_norm_rotary, qk_norm_rotary_forward, rotary, rotary_create, rotary_destroy,
                         rotary_forward, rotary_get_frequencies)
+from .blocks import (BlockNorm, Dense, block_norm, block_norm_forward, dense, dense_create, dense_destroy, dense_forward,
+                     dense_get_plan_info, dense_workspace_size)
+from .held import (HeldAttention, HeldStates, held_attention, held_attention_create, held_attention_destroy,
+                   held_attention_forward, held_attention_get_plan_info, held_attention_workspace_size, held_load,
+                   held_states_size, held_store)
 
 __all__ = ["conv2d_create", "conv2d_forward", "conv2d_destroy", "conv2d_get_plan_info",
            "conv2d_list_variants", "conv2d_create_variant", "conv2d_autotune",
@@ -31,7 +38,12 @@ __all__ = ["conv2d_create", "conv2d_forward", "conv2d_destroy", "conv2d_get_plan
            "rotary_create", "rotary_destroy", "rotary_get_frequencies", "rotary_forward", "qk_norm_rotary_forward",
            "cross_attention_create", "cross_attention_destroy", "cross_attention_workspace_size",
            "cross_attention_get_plan_info", "cross_attention_forward",
-           "Rotary", "CrossAttention", "rotary", "qk_norm_rotary", "cross_attention"]
+           "Rotary", "CrossAttention", "rotary", "qk_norm_rotary", "cross_attention",
+           "block_norm_forward", "dense_create", "dense_destroy", "dense_workspace_size", "dense_get_plan_info",
+           "dense_forward", "BlockNorm", "Dense", "block_norm", "dense",
+           "held_states_size", "held_store", "held_load", "held_attention_create", "held_attention_destroy",
+           "held_attention_workspace_size", "held_attention_get_plan_info", "held_attention_forward",
+           "HeldStates", "HeldAttention", "held_attention"]
 
 
 def load():

@@ -18,6 +18,9 @@ IS_ROTARY_HALF, IS_ROTARY_INTERLEAVED = 0, 1
 IS_ROTARY_UNSCALED, IS_ROTARY_LINEAR, IS_ROTARY_NTK, IS_ROTARY_RAMP = 0, 1, 2, 3
 IS_NORM_RMS, IS_NORM_LAYER = 1, 2
 IS_MAX_HEAD_DIM = 256
+IS_MAX_NORM_CHANNELS = 16384
+IS_ACT_NONE, IS_ACT_RELU, IS_ACT_GELU, IS_ACT_GELU_TANH, IS_ACT_SILU = 0, 1, 2, 3, 4
+IS_HELD_BLOCK = 32
 IS_MAX_CHAIN = 8
 IS_NOALLOC_MAX_WORKSPACE = 256 << 20
 
@@ -76,6 +79,34 @@ class cross_attention_desc(ctypes.Structure):
                [("mask_batch_stride", ctypes.c_int64)]
 
 
+class is_rows(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("len", ctypes.c_int), ("batch_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class block_norm_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("dtype", "c", "norm", "post")] + \
+               [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)] + \
+               [(f, is_rows) for f in ("x", "y", "x_out", "out")] + \
+               [(f, ctypes.c_int64) for f in ("gate_stride", "scale_stride", "shift_stride")]
+
+
+class dense_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("n", "len", "in_", "features", "dtype", "activation")] + \
+               [(f, ctypes.c_int64 * 2) for f in ("x_stride", "residual_stride", "out_stride")] + \
+               [("w_stride", ctypes.c_int64)]
+
+
+class held_states_desc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("n", "len", "heads", "d", "dtype")]
+
+
+class held_attention_desc(ctypes.Structure):
+    _fields_ = [("held", held_states_desc), ("lq", ctypes.c_int), ("hq", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+                ("mask_batch_stride", ctypes.c_int64)]
+
+
 # (name, restype, argtypes) of every function the header declares.
 _vp = ctypes.c_void_p
 SIGNATURES = [
@@ -109,6 +140,23 @@ SIGNATURES = [
     ("cross_attention_workspace_size", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
     ("cross_attention_get_plan_info", ctypes.c_int, [_vp, ctypes.POINTER(conv2d_plan_info)]),
     ("cross_attention_forward", ctypes.c_int, [_vp] * 9 + [ctypes.c_size_t, _vp]),
+    ("block_norm_forward", ctypes.c_int, [ctypes.POINTER(block_norm_desc)] + [_vp] * 11),
+    ("dense_create", ctypes.c_int, [ctypes.POINTER(dense_desc), ctypes.POINTER(_vp)]),
+    ("dense_destroy", None, [_vp]),
+    ("dense_workspace_size", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    ("dense_get_plan_info", ctypes.c_int, [_vp, ctypes.POINTER(conv2d_plan_info)]),
+    ("dense_forward", ctypes.c_int, [_vp] * 7 + [ctypes.c_size_t, _vp]),
+    ("held_states_size", ctypes.c_int, [ctypes.POINTER(held_states_desc), ctypes.POINTER(ctypes.c_size_t)]),
+    ("held_store", ctypes.c_int, [ctypes.POINTER(held_states_desc), ctypes.POINTER(is_tokens), _vp,
+                                  ctypes.POINTER(is_tokens), _vp, _vp, ctypes.c_int64, _vp, ctypes.c_int, _vp,
+                                  ctypes.c_size_t, _vp]),
+    ("held_load", ctypes.c_int, [ctypes.POINTER(held_states_desc), _vp, ctypes.c_size_t, ctypes.c_int,
+                                 ctypes.POINTER(is_tokens), _vp, ctypes.POINTER(is_tokens), _vp, _vp]),
+    ("held_attention_create", ctypes.c_int, [ctypes.POINTER(held_attention_desc), ctypes.POINTER(_vp)]),
+    ("held_attention_destroy", None, [_vp]),
+    ("held_attention_workspace_size", ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_size_t)]),
+    ("held_attention_get_plan_info", ctypes.c_int, [_vp, ctypes.POINTER(conv2d_plan_info)]),
+    ("held_attention_forward", ctypes.c_int, [_vp, _vp, _vp, ctypes.c_size_t] + [_vp] * 5 + [ctypes.c_size_t, _vp]),
     ("is_lds_tile_bytes", ctypes.c_size_t, [ctypes.c_int] * 6),
     ("is_swizzle_col", ctypes.c_int, [ctypes.c_int] * 5),
     ("is_persistent_grid", ctypes.c_int, [ctypes.c_int, ctypes.c_int]),

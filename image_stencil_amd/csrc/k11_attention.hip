@@ -41,6 +41,7 @@
 
 #include "attention.hpp"
 #include "common.hpp"
+#include "join.hpp"
 
 namespace is {
 namespace {
@@ -48,7 +49,6 @@ namespace {
 constexpr unsigned kOob = 0xFFFFFFF0u;
 constexpr float kLazy = 8.f;   // log2 of how far a row's maximum may outgrow M
 
-typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
 
@@ -860,59 +860,6 @@ __global__ __launch_bounds__(NW * 64, (Geo<DP, NW, SHARED, MASK>::WAVES)) void i
   }
 }
 
-// Joins the splits of a row. 2^log_sg neighbouring threads take 8 elements,
-// each the splits of its own, and exchange sums: with few rows, the latency of
-// reading one split after another would be all the time.
-template <typename T>
-__global__ __launch_bounds__(256) void is_k11_attention_join(const Args a, int tile_rows, int log_sg, int64_t items) {
-  typedef T T8 __attribute__((ext_vector_type(8)));
-  const int64_t thread = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int sg = threadIdx.x & ((1 << log_sg) - 1);
-  const int64_t it = thread >> log_sg;
-  if (it >= items) return;   // whole groups leave
-  const int chunks = a.d / 8, e = (int)(it % chunks) * 8;
-  const int64_t row = it / chunks;
-  const int r = (int)(row % a.rows), bh = (int)(row / a.rows);
-  const int rt = r / tile_rows, tr = r % tile_rows;
-  const int64_t step = (int64_t)a.row_tiles * tile_rows;
-  const int64_t at = ((int64_t)bh * a.splits * a.row_tiles + rt) * tile_rows + tr;
-  float top = -FLT_MAX, sum = 0.f, f[8] = {};
-  for (int i = sg; i < a.splits; i += 1 << log_sg) {
-    const float x = a.part_lse[at + i * step];
-    const floatx4 *p = reinterpret_cast<const floatx4 *>(a.part + (at + i * step) * a.d + e);
-    const floatx4 lo = p[0], hi = p[1];
-    const float next = fmaxf(top, x), old = __builtin_amdgcn_exp2f(top - next), w = __builtin_amdgcn_exp2f(x - next);
-    top = next;
-    sum = sum * old + w;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      f[u] = f[u] * old + w * lo[u];
-      f[4 + u] = f[4 + u] * old + w * hi[u];
-    }
-  }
-  float most = top;
-  for (int i = 0; i < log_sg; ++i) most = fmaxf(most, __shfl_xor(most, 1 << i));
-  const float scale = __builtin_amdgcn_exp2f(top - most);
-  sum *= scale;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) f[u] *= scale;
-  for (int i = 0; i < log_sg; ++i) {
-    sum += __shfl_xor(sum, 1 << i);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) f[u] += __shfl_xor(f[u], 1 << i);
-  }
-  if (sg != 0) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  T8 w;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) w[u] = (T)(f[u] * inv);
-  const int b = bh / a.hkv, i = r / a.group, h = bh % a.hkv * a.group + r % a.group;
-  *reinterpret_cast<T8 *>(static_cast<T *>(a.out) + b * a.os[0] + i * a.os[1] + h * a.os[2] + e) = w;
-  if (a.lse && e == 0)
-    a.lse[((int64_t)b * a.hq + h) * a.lq + i] =
-        sum == 0.f ? -INFINITY : (most + __log2f(sum)) * 0.69314718055994531f;
-}
-
 constexpr int kHeads[] = {32, 64, 96, 128, 160, 192, 256};   // padded head sizes
 
 // Calls f(std::integral_constant<int, DP>) for the plan's padded head size.
@@ -932,12 +879,6 @@ hipError_t for_head(int dp, F &&f) {
 constexpr int kResidentHead = 128;   // the largest padded head with a RESIDENT form
 constexpr int few_waves(int dp) { return dp <= 128 ? 4 : 2; }
 
-// Threads (log2) that join the splits of 8 elements.
-int join_group(int splits) {
-  int l = 0;
-  while (l < 5 && (1 << l) < splits) ++l;
-  return l;
-}
 int64_t join_items(const AttentionPlan &p) { return (int64_t)p.d.n * p.d.hkv * p.rows * (p.d.d / 8); }
 
 template <typename T>
@@ -958,10 +899,9 @@ hipError_t launch_t(const AttentionPlan &p, const Args &a, hipStream_t s) {
     return go(four{}, std::true_type{}, std::false_type{});
   });
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t items = join_items(p);
-  const int log_sg = join_group(p.splits);
-  return launch_kernel(is_k11_attention_join<T>, dim3((unsigned)(((items << log_sg) + 255) / 256)), dim3(256), 0, s, a,
-                       p.tile_rows, log_sg, items);
+  JoinArgs j = {a.part, a.part_lse, a.out, a.lse, {a.os[0], a.os[1], a.os[2]}, a.lq, a.hq, a.hkv, a.d, a.group, a.rows,
+                a.row_tiles, p.tile_rows, p.splits, join_group(p.splits), join_items(p)};
+  return launch_join<T>(j, s);
 }
 
 }  // namespace

@@ -1,0 +1,273 @@
+// k12_norm.hip -- the sum and norm between two blocks, one pass over rows of c
+// channels:
+//   x' = x + s g post(y),   z = norm(x') w (1 + scale) + shift + b
+// with both norms over the row (mean square, or mean and variance).
+//
+// A row belongs to TPR threads, NV vectors of 16 bytes each, and stays in
+// registers from its load to its stores: statistics are sums over the threads
+// (two for a norm with a mean, whose variance is that of the differences). What
+// multiplies and adds per channel is folded once for all rows of an entry:
+//   x' = x + G yhat,  G = s g post_weight;   z = A xhat + B,  A = w (1 + scale).
+// Groups of threads walk the rows of one entry, the next row's loads on their way
+// while this one is summed. Rows may start at any element (the memory path takes a vector
+// at any address); a vector across a row's end is taken by elements.
+#include <math.h>
+
+#include "blocks.hpp"
+#include "common.hpp"
+
+namespace is {
+namespace {
+
+struct Args {
+  NormPointers p;
+  int64_t xb, xr, yb, yr, xob, xor_, ob, orow, gate_b, scale_b, shift_b;
+  int entries, len, c, groups;   // groups of threads that share an entry's rows
+  int norm, post;
+  float eps, alpha, inv_c;
+};
+
+// The sum over the TPR threads of a row. Rows of one wave or less: lanes; else
+// the waves' sums meet in LDS, in two places in turn, so that one barrier is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *shared, int &turn) {
+#pragma unroll
+  for (int m = 1; m < (TPR < kWave ? TPR : kWave); m *= 2) v += __shfl_xor(v, m);
+  if constexpr (TPR > kWave) {
+    constexpr int W = TPR / kWave;
+    float *at = shared + turn * W;
+    turn ^= 1;
+    if ((threadIdx.x & (kWave - 1)) == 0) at[threadIdx.x / kWave] = v;
+    lds_barrier();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += at[i];
+  }
+  return v;
+}
+
+template <typename T, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void is_k12_block_norm(const Args a) {
+  constexpr int V = 16 / sizeof(T), BLOCK = TPR > 256 ? TPR : 256;
+  typedef T vec __attribute__((ext_vector_type(V)));
+  typedef T uvec __attribute__((ext_vector_type(V), aligned(sizeof(T))));   // at any element
+  __shared__ float shared[TPR > kWave ? 2 * TPR / kWave : 1];
+  lds_poison(shared, sizeof(shared));
+  int turn = 0;
+  const int lane = threadIdx.x % TPR;
+  const int64_t g = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
+  const int b = (int)(g / a.groups);
+  int i = (int)(g - (int64_t)b * a.groups);
+  if (b >= a.entries) return;     // whole groups of threads leave
+
+  // Vector v of a thread: elements at .. at + V - 1, the last one cut at c.
+  auto load = [&](const T *row, int v) -> vec {
+    const int at = (lane + v * TPR) * V;
+    vec r = {};
+    if (at + V <= a.c) {
+      r = *reinterpret_cast<const uvec *>(row + at);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (at + j < a.c) r[j] = row[at + j];
+    }
+    return r;
+  };
+  auto store = [&](T *row, int v, const float (&f)[V]) {
+    const int at = (lane + v * TPR) * V;
+    vec r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) r[j] = (T)f[j];
+    if (at + V <= a.c) {
+      *reinterpret_cast<uvec *>(row + at) = r;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (at + j < a.c) row[at + j] = r[j];
+    }
+  };
+  const T *x = static_cast<const T *>(a.p.x) + b * a.xb;
+  const T *y = static_cast<const T *>(a.p.y) + b * a.yb;
+  T *x_out = static_cast<T *>(a.p.x_out) + b * a.xob;
+  T *out = static_cast<T *>(a.p.out) + b * a.ob;
+  const bool has_y = a.p.y != nullptr;
+  vec rx[NV] = {}, ry[NV] = {};
+  auto fetch = [&](int row) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      rx[v] = load(x + row * a.xr, v);
+      if (has_y) ry[v] = load(y + row * a.yr, v);
+    }
+  };
+  fetch(i);
+
+  float G[NV][V], A[NV][V], B[NV][V];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = (lane + v * TPR) * V + j;
+      G[v][j] = a.alpha;
+      A[v][j] = 1.f;
+      B[v][j] = 0.f;
+      if (e < a.c) {
+        if (a.p.gate) G[v][j] *= (float)static_cast<const T *>(a.p.gate)[b * a.gate_b + e];
+        if (a.post && a.p.post_weight) G[v][j] *= a.p.post_weight[e];
+        if (a.p.weight) A[v][j] = a.p.weight[e];
+        if (a.p.scale) A[v][j] *= 1.f + (float)static_cast<const T *>(a.p.scale)[b * a.scale_b + e];
+        if (a.p.shift) B[v][j] = (float)static_cast<const T *>(a.p.shift)[b * a.shift_b + e];
+        if (a.p.bias) B[v][j] += a.p.bias[e];
+      }
+    }
+
+  // f in place normed: minus its mean (IS_NORM_LAYER), by its mean square.
+  auto normed = [&](float (&f)[NV][V], int kind) {
+    if (kind == IS_NORM_LAYER) {
+      float sum = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += f[v][j];
+      const float mean = row_sum<TPR>(sum, shared, turn) * a.inv_c;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[v][j] = (lane + v * TPR) * V + j < a.c ? f[v][j] - mean : 0.f;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum += f[v][j] * f[v][j];
+    const float inv = rsqrtf(row_sum<TPR>(sum, shared, turn) * a.inv_c + a.eps);   // also below the normal numbers
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[v][j] *= inv;
+  };
+
+  while (true) {
+    float f[NV][V], h[NV][V];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[v][j] = (float)rx[v][j];
+        h[v][j] = (float)ry[v][j];
+      }
+    const int row = i;
+    i += a.groups;
+    if (i < a.len) fetch(i);
+    if (has_y) {
+      if (a.post) normed(h, a.post);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[v][j] += G[v][j] * h[v][j];
+        if (a.p.x_out) store(x_out + row * a.xor_, v, f[v]);
+      }
+    }
+    if (a.norm) {
+      normed(f, a.norm);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[v][j] = f[v][j] * A[v][j] + B[v][j];
+        store(out + row * a.orow, v, f[v]);
+      }
+    }
+    if (i >= a.len) break;
+  }
+}
+
+// Threads of a row and their vectors, the fewest threads first.
+struct Shape {
+  int tpr, nv;
+};
+constexpr Shape kShapes[] = {{16, 1}, {64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4}, {512, 4}, {512, 8}};
+
+int shape_of(const block_norm_desc &d) {
+  const int v = d.dtype == IS_F32 ? 4 : 8;
+  int i = 0;
+  while ((int64_t)kShapes[i].tpr * kShapes[i].nv * v < d.c) ++i;
+  return i;
+}
+
+// Groups of threads that share an entry's rows: all rows at once while that is
+// less than the waves the chip holds, a few rows in turn beyond.
+int groups_of(const block_norm_desc &d) {
+  const Shape s = kShapes[shape_of(d)];
+  const double most = 4096.0 * kWave / s.tpr;
+  const double rows = (double)d.x.n * d.x.len;
+  const int each = rows <= most ? 1 : (int)ceil(rows / most);
+  const int groups = (d.x.len + each - 1) / each;
+  return groups < 1 ? 1 : groups;
+}
+
+int64_t blocks_of(const block_norm_desc &d) {
+  const Shape s = kShapes[shape_of(d)];
+  const int per = s.tpr > 256 ? 1 : 256 / s.tpr;
+  return ((int64_t)d.x.n * groups_of(d) + per - 1) / per;
+}
+
+template <typename T>
+hipError_t launch_t(const block_norm_desc &d, const Args &a, hipStream_t s) {
+  const dim3 grid((unsigned)blocks_of(d));
+  auto go = [&](auto tpr, auto nv) {
+    constexpr int TPR = decltype(tpr)::value;
+    return launch_kernel(is_k12_block_norm<T, TPR, decltype(nv)::value>, grid, dim3(TPR > 256 ? TPR : 256), 0, s, a);
+  };
+#define IS_SHAPE(TPR, NV) go(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{})
+  switch (shape_of(d)) {
+    case 0: return IS_SHAPE(16, 1);
+    case 1: return IS_SHAPE(64, 1);
+    case 2: return IS_SHAPE(64, 2);
+    case 3: return IS_SHAPE(64, 4);
+    case 4: return IS_SHAPE(256, 2);
+    case 5: return IS_SHAPE(256, 4);
+    case 6: return IS_SHAPE(512, 4);
+    default:
+      if constexpr (sizeof(T) == 4) return IS_SHAPE(512, 8);
+      return hipErrorInvalidValue;     // 16-bit rows end at the shape before
+  }
+#undef IS_SHAPE
+}
+
+}  // namespace
+
+double block_norm_threads(const block_norm_desc &d) {
+  const Shape s = kShapes[shape_of(d)];
+  return (double)blocks_of(d) * (s.tpr > 256 ? s.tpr : 256);
+}
+
+hipError_t launch_block_norm(const block_norm_desc &d, const NormPointers &p, hipStream_t s) {
+  Args a;
+  a.p = p;
+  a.xb = d.x.batch_stride;
+  a.xr = d.x.row_stride;
+  a.yb = p.y ? d.y.batch_stride : 0;
+  a.yr = p.y ? d.y.row_stride : 0;
+  a.xob = p.x_out ? d.x_out.batch_stride : 0;
+  a.xor_ = p.x_out ? d.x_out.row_stride : 0;
+  a.ob = p.out ? d.out.batch_stride : 0;
+  a.orow = p.out ? d.out.row_stride : 0;
+  a.gate_b = d.gate_stride;
+  a.scale_b = d.scale_stride;
+  a.shift_b = d.shift_stride;
+  a.entries = d.x.n;
+  a.len = d.x.len;
+  a.c = d.c;
+  a.groups = groups_of(d);
+  a.norm = d.norm;
+  a.post = d.post;
+  a.eps = d.eps;
+  a.alpha = d.residual_scale;
+  a.inv_c = 1.f / (float)d.c;
+  switch (d.dtype) {
+    case IS_F32: return launch_t<float>(d, a, s);
+    case IS_F16: return launch_t<_Float16>(d, a, s);
+    default: return launch_t<__bf16>(d, a, s);
+  }
+}
+
+}  // namespace is

@@ -473,6 +473,164 @@ is_status cross_attention_forward(cross_attention_plan plan, const void *q, cons
                                   const uint8_t *key_mask, const int32_t *key_lengths, void *out, float *lse,
                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the attention of a block: the sum and norm between two
+ * blocks, dense layers on tokens, and attention over states held in 8 bits. The
+ * conventions of the attention operators above hold.
+ *
+ * A row tensor is n x len rows of contiguous elements (n entries of len tokens,
+ * all heads of a token together); batch and row strides are free, as there.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int n, len;                         /* either may be 0: no work */
+  int64_t batch_stride, row_stride;   /* elements */
+} is_rows;
+
+#define IS_MAX_NORM_CHANNELS 16384
+
+/* Between two blocks, in one pass over rows of c channels: the residual stream x
+ * takes the last block's output y, and the next block's input is normed from it,
+ *     x_out = x + residual_scale * gate[b] * post(y)
+ *     out   = norm(x_out) * weight * (1 + scale[b]) + shift[b] + bias
+ * where post and norm are 0 (for post: y as it is; for norm: no out), IS_NORM_RMS
+ * or IS_NORM_LAYER over the c channels, post(y) times post_weight. The norm sees
+ * x_out before it is rounded.
+ *  dtype       : IS_F32, IS_F16 or IS_BF16 of x, y, x_out, out, gate, scale, shift
+ *  y           : NULL: no block before; x_out = x is not written (x_out NULL)
+ *  x_out       : NULL with y given: the sum is normed and not kept
+ *  gate, scale, shift: c values for every entry, entries gate_stride ... elements
+ *                apart (0: one row for all), or NULL for ones (gate) and zeros
+ *  post_weight, weight, bias: c fp32 values or NULL (ones; bias: zeros)
+ *  eps         : >= 0, finite; residual_scale: finite
+ * x_out and out may each be x or y itself with the same strides; otherwise
+ * outputs overlap nothing (IS_ERR_INVALID_ARG). Rows may start at any element;
+ * bases are 16-byte aligned, those of the vectors aligned to their type. Errors: also IS_ERR_UNSUPPORTED (c over IS_MAX_NORM_CHANNELS, dtype,
+ * sizes that need 2^32 or more threads). */
+typedef struct {
+  is_dtype dtype;
+  int c;
+  int norm, post;
+  float eps, residual_scale;
+  is_rows x, y, x_out, out;           /* sizes equal; those of absent tensors are not read */
+  int64_t gate_stride, scale_stride, shift_stride;
+} block_norm_desc;
+
+is_status block_norm_forward(const block_norm_desc *d, const void *x, const void *y, const void *gate,
+                             const float *post_weight, const float *weight, const float *bias, const void *scale,
+                             const void *shift, void *x_out, void *out, hipStream_t stream);
+
+/* Dense layer on tokens (a 1x1 convolution of any width on NHWC features):
+ *     out[r][f] = residual[r][f] + act( sum_i x[r][i] * w[f][i] + bias[f] )
+ * Activations: IS_ACT_GELU is x Phi(x) with the normal distribution's Phi,
+ * IS_ACT_GELU_TANH its form with tanh(sqrt(2/pi) (x + 0.044715 x^3)), IS_ACT_SILU
+ * is x / (1 + exp(-x)). At -infinity these three give their limit, zero.
+ *  in, features: k inputs, a multiple of 8 (IS_ERR_UNSUPPORTED), and any number
+ *               of outputs, both >= 1
+ *  dtype      : IS_F16 or IS_BF16 of x, w, residual and out
+ *  x          : n x len rows of `in`, w: `features` rows of `in`, w_stride elements
+ *               apart; strides multiples of 8 (IS_ERR_MISALIGNED), row strides at
+ *               most 2^21
+ *  residual   : n x len rows of `features` or absent (at forward: NULL), with
+ *               strides of its own; it may be out itself with the same strides
+ *  bias       : `features` fp32 values or NULL
+ * Sums are fp32; bias, activation and residual are applied to the sum in fp32 and
+ * the result is rounded once. */
+typedef enum {
+  IS_ACT_NONE = 0,
+  IS_ACT_RELU = 1,
+  IS_ACT_GELU = 2,
+  IS_ACT_GELU_TANH = 3,
+  IS_ACT_SILU = 4
+} is_activation;
+
+typedef struct {
+  int n, len, in, features;
+  is_dtype dtype;
+  is_activation activation;
+  int64_t x_stride[2], residual_stride[2], out_stride[2];   /* batch, row; elements */
+  int64_t w_stride;
+} dense_desc;
+
+typedef struct dense_plan_s *dense_plan;
+
+/* Check a descriptor and choose a kernel. Host only; immutable, shared by threads
+ * and streams. Errors: IS_ERR_INVALID_ARG, IS_ERR_UNSUPPORTED, IS_ERR_MISALIGNED,
+ * IS_ERR_NO_MEMORY. */
+is_status dense_create(const dense_desc *d, dense_plan *out);
+void dense_destroy(dense_plan plan);
+
+/* Device bytes of workspace: 0 unless few rows and features meet long sums, which
+ * are then split over workgroups and joined. */
+is_status dense_workspace_size(dense_plan plan, size_t *bytes);
+is_status dense_get_plan_info(dense_plan plan, conv2d_plan_info *info);
+
+/* Enqueue on `stream`. x and w may be NULL when they have no element; the
+ * workspace as for cross_attention_forward. out and workspace overlap neither
+ * the inputs (but for residual == out) nor each other (IS_ERR_INVALID_ARG). */
+is_status dense_forward(dense_plan plan, const void *x, const void *w, const float *bias, const void *residual,
+                        void *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* States held in 8 bits: the keys and values that a cross attention reads many
+ * times, as e4m3 numbers (4 exponent and 3 fraction bits, at most 448) times a
+ * power of two for every block of IS_HELD_BLOCK tokens and head, k and v apart:
+ * 2^e with the smallest e >= -120 for which no finite number of the block
+ * exceeds 448 * 2^e. Numbers are rounded to nearest even; one that this would
+ * take past the data type's largest number becomes 240 * 2^e, and infinities and
+ * NaN are held as NaN (they do not count for e). What is held is a number of the data
+ * type: loading it is exact.
+ * The store is device memory of held_states_size bytes, in an order of the
+ * library's own (the operands of the matrix cores), heads padded to a multiple
+ * of 32 elements:
+ *  n, len, heads, d: entries, tokens (a capacity), key heads, elements (a multiple
+ *              of 8, 8 .. IS_MAX_HEAD_DIM); n and len may be 0
+ *  dtype     : IS_F16 or IS_BF16 of what is stored and of the queries
+ * held_store puts k and v (n x kt.len tokens) at tokens at .. at + kt.len - 1 of
+ * every entry; `at` is a multiple of IS_HELD_BLOCK. It writes whole blocks: the
+ * rest of the last one becomes zeros, other blocks keep what they hold. Tokens
+ * beyond key_lengths[b] (if given; counted from `at`, clamped) or with a zero in
+ * key_mask (if given; n x kt.len bytes, rows key_mask_stride apart) are not looked at and
+ * held as zeros. held_load gives back tokens at .. at + kt.len - 1 (any `at`).
+ * Strides of k and v are free; no two elements of an output share an address.
+ * Errors: IS_ERR_INVALID_ARG (sizes, `at`, overlaps), IS_ERR_MISALIGNED (bases,
+ * the store's base to 16 bytes), IS_ERR_UNSUPPORTED, IS_ERR_WORKSPACE (a store
+ * smaller than needed). */
+#define IS_HELD_BLOCK 32
+
+typedef struct {
+  int n, len, heads, d;
+  is_dtype dtype;
+} held_states_desc;
+
+is_status held_states_size(const held_states_desc *d, size_t *bytes);
+is_status held_store(const held_states_desc *d, const is_tokens *kt, const void *k, const is_tokens *vt, const void *v,
+                     const uint8_t *key_mask, int64_t key_mask_stride, const int32_t *key_lengths, int at, void *held,
+                     size_t held_bytes, hipStream_t stream);
+is_status held_load(const held_states_desc *d, const void *held, size_t held_bytes, int at, const is_tokens *kt,
+                    void *k, const is_tokens *vt, void *v, hipStream_t stream);
+
+/* Cross attention to held states: what cross_attention_forward gives on the
+ * tensors that held_load gives, over all `len` tokens of the store or those that
+ * key_lengths and key_mask leave; masked tokens may never have been stored.
+ *  lq, hq     : queries of an entry and query heads, hq % held.heads == 0
+ *  scale, strides of q and out, masks, lse and workspace: as for cross_attention_* */
+typedef struct {
+  held_states_desc held;
+  int lq, hq;
+  float scale;
+  int64_t q_stride[3], out_stride[3];
+  int64_t mask_batch_stride;
+} held_attention_desc;
+
+typedef struct held_attention_plan_s *held_attention_plan;
+
+is_status held_attention_create(const held_attention_desc *d, held_attention_plan *out);
+void held_attention_destroy(held_attention_plan plan);
+is_status held_attention_workspace_size(held_attention_plan plan, size_t *bytes);
+is_status held_attention_get_plan_info(held_attention_plan plan, conv2d_plan_info *info);
+is_status held_attention_forward(held_attention_plan plan, const void *q, const void *held, size_t held_bytes,
+                                 const uint8_t *key_mask, const int32_t *key_lengths, void *out, float *lse,
+                                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* LDS bytes of an input tile that covers tile_w x tile_h outputs of a filter
  * r x s over `channels` channels of `elem_bytes` each: the tile plus its halo,
  * (tile_w + s - 1) * (tile_h + r - 1) * channels * elem_bytes. The sizing rule
