@@ -11,9 +11,11 @@ typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
 
 constexpr unsigned kOutside = 0xFFFFFFF0u;   // an offset outside every buffer: zeros
 
-// A buffer of `bytes` at `at`. An offset (unsigned) that is not inside reads zeros.
+// A buffer of `bytes` at `at` (both alike in all lanes). An offset (unsigned) that is not inside reads zeros.
 __device__ __forceinline__ uintx4 buffer_at(uint64_t at, unsigned bytes) {
-  return uintx4{(unsigned)at, (unsigned)(at >> 32) & 0xffffu, bytes, (unsigned)kBufferFlags};
+  return uintx4{(unsigned)__builtin_amdgcn_readfirstlane((unsigned)at),
+                (unsigned)__builtin_amdgcn_readfirstlane((unsigned)(at >> 32) & 0xffffu),
+                (unsigned)__builtin_amdgcn_readfirstlane(bytes), (unsigned)kBufferFlags};
 }
 
 // N operations of 16 bytes per lane, operation i to dst + 1024 i + 16 lane of LDS.
@@ -48,6 +50,14 @@ __device__ __forceinline__ void load_lds16(uintx4 rs, unsigned dst, const unsign
 }
 #undef IS_LOAD16
 #undef IS_NEXT
+
+// One operation of 4 bytes per lane.
+__device__ __forceinline__ void load_lds4(uintx4 rs, unsigned dst, unsigned off) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                   :
+                   : "s"(dst), "v"(off), "s"(rs)
+                   : "memory");
+}
 
 // Until at most N of this wave's vector-memory operations are outstanding.
 template <int N>

@@ -41,6 +41,7 @@
 
 #include "attention.hpp"
 #include "common.hpp"
+#include "divide.hpp"
 #include "join.hpp"
 
 namespace is {
@@ -51,21 +52,6 @@ constexpr float kLazy = 8.f;   // log2 of how far a row's maximum may outgrow M
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
-
-// n / d for 0 <= n < 2^31 by a product: with 2^(s - 1) < d <= 2^s and
-// m = ceil(2^(31 + s) / d), n m >> 31 + s is exact. (The index arithmetic of a
-// workgroup would otherwise spend four divisions before its first load.)
-struct Divisor {
-  unsigned m, s;
-};
-Divisor divisor(unsigned d) {
-  unsigned s = 0;
-  while (((uint64_t)1 << s) < d) ++s;
-  return {(unsigned)((((uint64_t)1 << (31 + s)) + d - 1) / d), s};
-}
-__device__ __forceinline__ int divide(int n, Divisor d) {
-  return (int)(((uint64_t)(unsigned)n * d.m) >> (31 + d.s));
-}
 
 struct Args {
   const void *q, *k, *v;

@@ -114,7 +114,10 @@ def test_strides(rows):
     say("dense strides", rows)
     n, k, m = 3, 72, 50
     x, w, b, r = (t.cuda() for t in _case(n, rows, k, m, F16, seed=rows))
-    want = isa.dense(x, w, b, "silu", r)
+    exact = bo.dense(x.cpu(), w.cpu(), b.cpu(), "silu", r.cpu())
+
+    def check(got, want=None):     # (another layout may take another kernel, and so other bits)
+        _check(got, *(want or exact), "strides")
     wide = torch.zeros(n, rows, 2 * k + 8, dtype=F16, device="cuda")
     wide[:, :, k:2 * k] = x
     ww = torch.zeros(m, k + 16, dtype=F16, device="cuda")
@@ -124,18 +127,18 @@ def test_strides(rows):
     res = torch.zeros(n, rows, m + 1, dtype=F16, device="cuda")
     res[:, :, :m] = r
     plan = isa.Dense(wide[:, :, k:2 * k], ww[:, 8:8 + k], out=out, residual=res[:, :, :m], activation="silu")
-    assert torch.equal(plan.forward(wide[:, :, k:2 * k], ww[:, 8:8 + k], b, res[:, :, :m], out), want)
+    check(plan.forward(wide[:, :, k:2 * k], ww[:, 8:8 + k], b, res[:, :, :m], out))
     assert (big[:, rows:] == 5).all() and (big[:, :, m:] == 5).all()
     swapped = torch.zeros(rows, n, k, dtype=F16, device="cuda")     # rows of the entries alternate
     swapped.copy_(x.transpose(0, 1))
-    assert torch.equal(isa.dense(swapped.transpose(0, 1), w, b, "silu", r), want)
-    one = isa.dense(x[:1].expand(n, -1, -1), w, b, "silu", r)       # entries repeated
-    assert torch.equal(one, isa.dense(x[:1].repeat(n, 1, 1), w, b, "silu", r))
-    same = isa.dense(x[:, :1].expand(-1, rows, -1), w, b, "silu", r)
-    assert torch.equal(same, isa.dense(x[:, :1].repeat(1, rows, 1), w, b, "silu", r))
+    check(isa.dense(swapped.transpose(0, 1), w, b, "silu", r))
+    one = x[:1].cpu().repeat(n, 1, 1)                                # entries repeated
+    check(isa.dense(x[:1].expand(n, -1, -1), w, b, "silu", r), bo.dense(one, w.cpu(), b.cpu(), "silu", r.cpu()))
+    same = x[:, :1].cpu().repeat(1, rows, 1)                         # rows repeated
+    check(isa.dense(x[:, :1].expand(-1, rows, -1), w, b, "silu", r), bo.dense(same, w.cpu(), b.cpu(), "silu", r.cpu()))
     place = r.clone()
     plan = isa.Dense(x, w, out=place, residual=place, activation="silu")
-    assert torch.equal(plan.forward(x, w, b, place, place), want)
+    check(plan.forward(x, w, b, place, place))
 
 
 def test_rows_are_independent_and_repeatable():
