@@ -1,12 +1,14 @@
 // k14_held.hip -- keys and values into 8 bits and back.
 //
-// A workgroup takes one block of 32 tokens of one entry and head, keys then values:
-// each thread has 8 neighbouring elements of a token, so that reads and writes
-// of the caller's tensor are whole rows of a head. The scale is the power of two
-// that brings the largest finite magnitude to 448 or under, taken from its exponent
-// and fraction bits, so that quotients are exact and rounding is that of the
-// conversion to e4m3 alone. The record is put together in LDS and leaves in whole
-// lines.
+// A workgroup takes one block of 32 tokens of one entry and head: two waves its keys, two
+// its values, all loads first. A key thread has 8 neighbouring elements of a token at a
+// time, a value thread those of four tokens, which are neighbours in the record, so that
+// both touch the caller's tensor in whole rows of a head and put words, not bytes,
+// together. The scale is the power of two that brings the largest finite magnitude to
+// 448 or under, taken from its exponent and fraction bits, so that quotients are exact and
+// rounding is that of the conversion to e4m3 alone. The record is put together in LDS
+// (16-byte slots permuted, so that lanes a row apart meet different banks) and
+// leaves in whole lines.
 #include <math.h>
 
 #include "common.hpp"
@@ -40,81 +42,124 @@ __device__ __forceinline__ int value_byte(int token, int e) {
 template <typename T>
 __device__ __forceinline__ constexpr int top_exponent() { return sizeof(T) == 2 && __is_same(T, _Float16) ? 8 : 120; }
 
-// Largest magnitude of the workgroup.
-__device__ __forceinline__ float block_max(float v, float *shared) {
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v = fmaxf(v, __shfl_xor(v, m));
-  if ((threadIdx.x & (kWave - 1)) == 0) shared[threadIdx.x / kWave] = v;
-  __syncthreads();
-  return fmaxf(fmaxf(shared[0], shared[1]), fmaxf(shared[2], shared[3]));
+// Slots of 16 bytes of a record while it is put together: token t of a key piece p, element
+// e of a value half lie in another place of their 8.
+__device__ __forceinline__ int key_slot(int piece, int token) { return piece * 32 + (token ^ (piece & 7)); }
+__device__ __forceinline__ int value_slot(int half, int e) {
+  return (e >> 5) * 64 + half * 32 + ((e & 31) ^ ((e >> 3) & 7));
 }
 
-// DP: d padded. A thread holds NV vectors of 8 elements.
+// The largest finite magnitude.
+template <typename V>
+__device__ __forceinline__ float most_of(const V &x, float most) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = fabsf((float)x[j]);
+    if (m < INFINITY) most = fmaxf(most, m);
+  }
+  return most;
+}
+
+// 8 numbers times inv as e4m3, at most cap: one that is none becomes NaN.
+template <typename V>
+__device__ __forceinline__ uintx2 e4m3(const V &x, float inv, float cap) {
+  float z[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float f = (float)x[j];
+    z[j] = fabsf(f) < INFINITY ? fminf(fmaxf(f * inv, -cap), cap) : NAN;
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(z[4], z[5], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(z[6], z[7], hi, true);
+  return uintx2{(unsigned)lo, (unsigned)hi};
+}
+
+// DP: d padded.
 template <typename T, int DP>
 __global__ __launch_bounds__(kThreads) void is_k14_held_store(const Args a) {
   typedef T uvec __attribute__((ext_vector_type(8), aligned(sizeof(T))));   // at any element
-  constexpr int CH = DP / 8, NV = (32 * CH + kThreads - 1) / kThreads;
-  __shared__ __attribute__((aligned(16))) char record[32 * DP];
-  __shared__ float shared[2][4];
+  constexpr int CH = DP / 8, HALF = kThreads / 2;
+  constexpr int NK = 32 * CH / HALF;                         // vectors of a key thread
+  constexpr int NG = (8 * CH + HALF - 1) / HALF;             // token fours of a value thread
+  constexpr int NV = NK > 4 * NG ? NK : 4 * NG;
+  __shared__ __attribute__((aligned(16))) uintx4 record[4 * DP];
+  __shared__ float shared[4];
   lds_poison(record, sizeof(record));
-  const int per = a.blocks, blk = blockIdx.x % per, bh = blockIdx.x / per, b = bh / a.heads, h = bh % a.heads;
+  // Neighbouring workgroups: the heads of the same tokens, which lie together in memory.
+  const int h = blockIdx.x % a.heads, rest = blockIdx.x / a.heads, blk = rest % a.blocks, b = rest / a.blocks;
+  const int bh = b * a.heads + h;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), side = wave >> 1, thread = threadIdx.x & (HALF - 1);
   int len = a.len;
   if (a.lengths) len = min(len, max(0, a.lengths[b]));
   const int64_t rec = (int64_t)bh * a.capacity_blocks + a.at / 32 + blk;
+  const HeldSide &t = a.side[side];
+  const T *p = static_cast<const T *>(t.p) + b * t.batch + h * t.head;
+  auto vector = [&](int token, int e) -> uvec {
+    const int at = blk * 32 + token;
+    bool in = e < a.d && at < len;
+    if (in && a.mask) in = a.mask[b * a.mask_stride + at] != 0;
+    return in ? *reinterpret_cast<const uvec *>(p + at * t.token + e) : uvec{};
+  };
+  // Key vector i: token item / CH. Value four i: tokens 8 a + 4 half + (0..3) of group 2 a + half.
+  uvec x[NV];
+  float most = 0.f;
+  if (side == 0) {
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const HeldSide &t = a.side[side];
-    const T *p = static_cast<const T *>(t.p) + b * t.batch + h * t.head;
-    float f[NV][8];
-    float most = 0.f;
+    for (int i = 0; i < NK; ++i) x[i] = vector((thread + i * HALF) / CH, (thread + i * HALF) % CH * 8);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int item = threadIdx.x + i * kThreads, token = item / CH, e = item % CH * 8, at = blk * 32 + token;
-      bool in = item < 32 * CH && e < a.d && at < len;
-      if (in && a.mask) in = a.mask[b * a.mask_stride + at] != 0;
-      uvec x = {};
-      if (in) x = *reinterpret_cast<const uvec *>(p + at * t.token + e);
+    for (int i = 0; i < NK; ++i) most = most_of(x[i], most);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[i][j] = (float)x[j];
-        const float m = fabsf(f[i][j]);
-        if (m < INFINITY) most = fmaxf(most, m);
-      }
+    for (int i = 0; i < 4 * NG; ++i) {
+      const int item = thread + i / 4 * HALF;
+      x[i] = item < 8 * CH ? vector(item / CH * 4 + i % 4, item % CH * 8) : uvec{};
     }
-    most = block_max(most, shared[side]);
-    // most = 1.f 2^(E - 127) = (1.f / 2) 2^(E - 126), and 448 = (1.75 / 2) 2^9.
-    const unsigned bits = __float_as_uint(most);
-    int e2 = (int)(bits >> 23) - ((bits & 0x7fffffu) <= 0x600000u ? 135 : 134);
-    e2 = max(e2, -120);
-    const float scale = __uint_as_float((unsigned)(e2 + 127) << 23), inv = __uint_as_float((unsigned)(127 - e2) << 23);
-    const float cap = e2 == top_exponent<T>() ? 240.f : 448.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int item = threadIdx.x + i * kThreads, token = item / CH, e = item % CH * 8;
-      if (item >= 32 * CH) continue;
-      float z[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = f[i][j] * inv;
-        z[j] = fabsf(f[i][j]) < INFINITY ? fminf(fmaxf(q, -cap), cap) : NAN;
-      }
-      int lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(z[4], z[5], 0, false);
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], lo, true);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(z[6], z[7], hi, true);
-      if (side == 0) {
-        *reinterpret_cast<uintx2 *>(record + key_byte(token, e)) = uintx2{(unsigned)lo, (unsigned)hi};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) record[value_byte(token, e + j)] = (char)((j < 4 ? lo : hi) >> (8 * (j & 3)));
-      }
-    }
-    __syncthreads();
-    char *to = a.held + rec * 64 * DP + side * 32 * DP;
-    for (int i = threadIdx.x; i < 2 * DP; i += kThreads)
-      *reinterpret_cast<uintx4 *>(to + i * 16) = *reinterpret_cast<const uintx4 *>(record + i * 16);
-    if (threadIdx.x == 0) *reinterpret_cast<float *>(a.held + a.scales_at + (rec * 2 + side) * 4) = scale;
-    __syncthreads();
+    for (int i = 0; i < 4 * NG; ++i) most = most_of(x[i], most);
   }
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
+  if ((threadIdx.x & (kWave - 1)) == 0) shared[wave] = most;
+  __syncthreads();
+  most = fmaxf(shared[2 * side], shared[2 * side + 1]);
+  // most = 1.f 2^(E - 127) = (1.f / 2) 2^(E - 126), and 448 = (1.75 / 2) 2^9.
+  const unsigned bits = __float_as_uint(most);
+  int e2 = (int)(bits >> 23) - ((bits & 0x7fffffu) <= 0x600000u ? 135 : 134);
+  e2 = max(e2, -120);
+  const float scale = __uint_as_float((unsigned)(e2 + 127) << 23), inv = __uint_as_float((unsigned)(127 - e2) << 23);
+  const float cap = e2 == top_exponent<T>() ? 240.f : 448.f;
+  if (side == 0) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int item = thread + i * HALF, token = item / CH, e = item % CH * 8;
+      reinterpret_cast<uintx2 *>(record + key_slot(e >> 4, token))[e >> 3 & 1] = e4m3(x[i], inv, cap);
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int item = thread + g * HALF, group = item / CH, e = item % CH * 8;
+      if (item >= 8 * CH) continue;
+      uintx2 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = e4m3(x[4 * g + i], inv, cap);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {      // byte j % 4 of the four tokens' words
+        const unsigned pick = (j & 3) | (4 + (j & 3)) << 8;
+        const unsigned lo = __builtin_amdgcn_perm(w[1][j / 4], w[0][j / 4], pick);
+        const unsigned hi = __builtin_amdgcn_perm(w[3][j / 4], w[2][j / 4], pick);
+        reinterpret_cast<unsigned *>(record + 2 * DP + value_slot(group & 1, e + j))[group >> 1] =
+            __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      }
+    }
+  }
+  __syncthreads();
+  uintx4 *to = reinterpret_cast<uintx4 *>(a.held + rec * 64 * DP);
+  for (int i = threadIdx.x; i < 4 * DP; i += kThreads) {
+    const int v = i - 2 * DP;
+    to[i] = record[i < 2 * DP ? key_slot(i / 32, i % 32) : 2 * DP + value_slot(v / 32 & 1, v / 64 * 32 + v % 32)];
+  }
+  if (thread == 0) *reinterpret_cast<float *>(a.held + a.scales_at + (rec * 2 + side) * 4) = scale;
 }
 
 template <typename T, int DP>
@@ -124,7 +169,8 @@ __global__ __launch_bounds__(kThreads) void is_k14_held_load(const Args a) {
   constexpr int CH = DP / 8;
   __shared__ __attribute__((aligned(16))) char record[64 * DP];
   lds_poison(record, sizeof(record));
-  const int per = a.blocks, blk = a.at / 32 + blockIdx.x % per, bh = blockIdx.x / per, b = bh / a.heads, h = bh % a.heads;
+  const int h = blockIdx.x % a.heads, rest = blockIdx.x / a.heads, blk = a.at / 32 + rest % a.blocks, b = rest / a.blocks;
+  const int bh = b * a.heads + h;
   const int64_t rec = (int64_t)bh * a.capacity_blocks + blk;
   const char *from = a.held + rec * 64 * DP;
   for (int i = threadIdx.x; i < 4 * DP; i += kThreads)

@@ -3,8 +3,8 @@
 //   out = softmax(scale q k^T) v,  k and v = e4m3 numbers times a power of two for
 //   each block of 32 keys.
 //
-// Few rows (is_k15_held_attention): the read of the held bytes is the work. Each wave
-// walks blocks of its own for the same 32 rows. A record holds the operands as the
+// Up to some thousand rows (is_k15_held_attention): each wave walks blocks of its own for
+// the same 32 rows; with few, the read of the held bytes is all the work. A record holds the operands as the
 // lanes need them, so they go from memory to registers in pieces of 1 KB, are
 // converted there (two numbers and their scale an instruction, exactly) and multiplied;
 // LDS only joins the waves at the end. Products, running maximum and the
@@ -313,7 +313,13 @@ bool configure_held(HeldPlan &p) {
   p.rows = d.lq * p.group;
   p.row_tiles = (p.rows + 31) / 32;
   const int64_t blocks = held_blocks(h.len), units = (int64_t)h.n * h.heads * p.row_tiles;
-  p.direct = p.rows <= 64;
+  // The held bytes directly up to four workgroups a CU's pair of slots (heads over 128: one
+  // slot); beyond, the products take so long that loading the states first for the faster
+  // kernel pays. Direct and loaded: 2 entries x 8 heads of 64 over 3600 keys, 3600 rows (1808
+  // workgroups) 81.8 and 79.8 us, 1024 rows (512) 25.5 and 40.2; 4 x 2 heads of 128 over 4096
+  // keys, 4096 rows (1024) 80.8 and 80.2, 8192 rows 160 and 136; 2 heads of 256 over 2000 keys,
+  // 8192 rows (512) 58 and 64, 14400 rows 109 and 81.
+  p.direct = units <= (held_padded(h.d) <= 128 ? 1024 : 512);
   p.splits = 1;
   p.split_blocks = (int)(blocks < 1 ? 1 : blocks);
   p.workgroups = units;
@@ -324,10 +330,18 @@ bool configure_held(HeldPlan &p) {
     return hipSuccess;
   });
   if (p.direct) {
-    // Two workgroups a CU, and at least four blocks a wave.
-    int64_t splits = units > 0 ? 512 / units : 1;
-    const int64_t most = blocks / (4 * kWaves);
-    splits = splits > most ? most : splits;
+    // A workgroup a CU, and at least two blocks a wave. (One token for each of 4 entries
+    // over 32771 keys, 2 heads of 128: 32 parts 18.5 us with the join, 61 parts 19.0, 114
+    // parts 22.2; 1000 keys, 4 heads of 128: 8 parts 7.7, none 8.2.) Several row tiles and
+    // heads to 128, where the products are the work: two a CU if that leaves a wave 16 blocks
+    // (1024 rows over 16384 keys, 8 heads of 64: 56 us, one a CU 81; but 512 rows over 3600
+    // keys, 16 heads: 19.7 and 17.1).
+    auto parts = [&](int64_t groups, int64_t each) {
+      const int64_t n = units > 0 ? groups / units : 1, most = blocks / (each * kWaves);
+      return n < most ? n : most;
+    };
+    int64_t splits = parts(256, 2);
+    if (p.row_tiles > 1 && held_padded(h.d) <= 128 && parts(512, 16) > splits) splits = parts(512, 16);
     if (splits > 1) {
       p.split_blocks = (int)((blocks + splits - 1) / splits);
       p.splits = (int)((blocks + p.split_blocks - 1) / p.split_blocks);
