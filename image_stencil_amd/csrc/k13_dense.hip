@@ -4,19 +4,29 @@
 // so that a lane's results are consecutive features of one token.
 //
 // Many rows (is_k13_dense): a workgroup of WF x WT waves computes tiles of 32 FB WF
-// features x 32 TB WT tokens with v_mfma_f32_32x32x16. Steps of 64 inputs of both
-// operands lie in LDS in two buffers, brought by DMA without passing registers: a
+// features x 32 TB WT tokens with v_mfma_f32_32x32x16, one after another. A step is 64
+// inputs of both operands, brought to LDS by DMA without passing registers: a
 // 128-byte row in 8 chunks of 16 bytes, chunk c of row r in slot c ^ ((r >> 1) & 7),
 // so that 16 lanes reading one chunk of 16 rows meet 16 different bank groups. The
-// last quarter of a step runs after the barrier that frees its buffer: its products
-// cover the first operand reads of the next step, whose data the barrier has
-// waited for, and the loads of the step after go out there. Results pass LDS as
-// fp32 once, a wave's own part, so that residual and output are touched in whole
-// rows of the wave's features.
+// weights' and the tokens' halves of the steps go round five LDS slots, which keeps loads
+// one and a half steps ahead, also from one tile to the next. The last quarter of a step
+// runs after the barrier that frees its slots: its products cover the first operand reads
+// of the next step. Results pass the one free slot as fp32, a wave's own part, so that
+// residual and output are touched by 4 lanes a token; nothing waits for their stores.
 //
 // Few rows (is_k13_dense_few): the weights are read once, straight into registers,
 // 16 features x 32 inputs an instruction (v_mfma_f32_16x16x32); the waves of a
 // workgroup take the inner sum in turn and join in LDS.
+//
+// What bounds it, measured on MI355Xs (bf16, inputs changing from call to call): 65536
+// rows, 4096 to 1024, with residual: 448 to 468 us, 1.17 to 1.23 PFLOP/s; 8192 cubed 809
+// to 841, 1.31 to 1.36 PFLOP/s: matrix cores 77% busy at 1.4 to 1.7 GHz, which the power
+// limit sets (a library product without residual: 377 and 690). Two 3600-token frames, 512
+// to 2048, GELU: 27.3 to 28.5; 8 steps are 12.4 of it, the activations and the write of a
+// whole tile per CU most of the rest. 16 rows, 8192 to 8192: 33, 4.1 TB/s (one row 28): the
+// 16 rows of x, read again by each workgroup, are as many requests as half the weights.
+// Steps that were taken back: touching the lines of later steps (a dword of each, 892 to
+// 1050); both quarters of an accumulator's half step one after the other (841 to 874).
 #include <math.h>
 
 #include "blocks.hpp"
@@ -260,9 +270,9 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
     });
   };
   // Operands or loads dealt to the products: those of slot u.
-  auto deal = [](auto u, auto count, auto &&f) {
-    constexpr int U = decltype(u)::value, N = decltype(count)::value;
-    constexpr int PER = (N + PRODUCTS - 1) / PRODUCTS;
+  auto deal = [](auto u, auto count, auto slots, auto &&f) {
+    constexpr int U = decltype(u)::value, N = decltype(count)::value, S = decltype(slots)::value;
+    constexpr int PER = (N + S - 1) / S;
     static_for<PER>([&](auto i) {
       constexpr int I = U * PER + decltype(i)::value;
       if constexpr (I < N) f(std::integral_constant<int, I>{});
@@ -270,6 +280,8 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
   };
   using Operands = std::integral_constant<int, OPERANDS>;
   using Loads = std::integral_constant<int, NI>;
+  using Slots = std::integral_constant<int, PRODUCTS>;
+  using Early = std::integral_constant<int, (PRODUCTS + 1) / 2>;
 
   // ---- Results: lane = token n32 of block j, features 32 i + 8 u + 4 half + (0..3). A
   // wave brings 32 features of 32 tokens at a time through LDS, so that residual and
@@ -419,8 +431,8 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
       static_for<3>([&](auto kk) {
         constexpr int KK = decltype(kk)::value;
         products(KK, [&](auto u) {
-          deal(u, Operands{}, [&](auto o) { read(ws, xs, KK + 1, o); });
-          if constexpr (KK == 0) deal(u, Loads{}, [&](auto i) { ask(w, i); });
+          deal(u, Operands{}, Early{}, [&](auto o) { read(ws, xs, KK + 1, o); });
+          if constexpr (KK == 0) deal(u, Loads{}, Slots{}, [&](auto i) { ask(w, i); });
         });
       });
       loads_left<NI>();      // the next step has arrived (this wave's part; W of the one after need not)
@@ -431,8 +443,8 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
       if (xs >= G::SLOTS * G::SLOT) xs -= G::SLOTS * G::SLOT;
       next(x, false);
       products(3, [&](auto u) {
-        deal(u, Operands{}, [&](auto o) { read(ws, xs, 0, o); });
-        deal(u, Loads{}, [&](auto i) { ask(x, i); });
+        deal(u, Operands{}, Early{}, [&](auto o) { read(ws, xs, 0, o); });
+        deal(u, Loads{}, Slots{}, [&](auto i) { ask(x, i); });
       });
     }
     // The results pass the slot that W's next loads will take, a wave's own part of it.
