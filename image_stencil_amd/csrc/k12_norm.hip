@@ -234,8 +234,9 @@ int groups_of(const block_norm_desc &d) {
   const Shape s = kShapes[shape_of(d)];
   const double rows = (double)d.x.n * d.x.len, waves = s.tpr / (double)kWave;
   const double most = (s.e <= 8 || rows * waves <= 4096.0 ? 4096.0 : 2048.0) / waves;
-  const int each = rows <= most ? 1 : (int)ceil(rows / most);
-  const int groups = (d.x.len + each - 1) / each;
+  double each = rows <= most ? 1.0 : ceil(rows / most);
+  if (each > d.x.len) each = d.x.len;
+  const int groups = (int)ceil(d.x.len / each);
   return groups < 1 ? 1 : groups;
 }
 

@@ -9,6 +9,11 @@
 // rounding is that of the conversion to e4m3 alone. The record is put together in LDS
 // (16-byte slots permuted, so that lanes a row apart meet different banks) and
 // leaves in whole lines.
+//
+// Bound: one read of the states and one write of half their bytes, and back. 4 entries of
+// 16384 tokens, 4 heads of 128, bf16, put and got: 93 us, 4.3 TB/s (a copy's rate: 80), of
+// which the load 40 (5.0 TB/s) and the store about 50: its workgroups, of 24 KB each,
+// load, reduce and store in turn. (Single bytes to LDS in place of words of four tokens: 57.)
 #include <math.h>
 
 #include "common.hpp"

@@ -10,8 +10,13 @@
 // LDS only joins the waves at the end. Products, running maximum and the
 // order of keys are those of the cross attention kernel:
 //   S^T (keys x rows) = K Q^T,   O^T (d x rows) = V^T P^T.
-// Many rows: the states are loaded into the workspace once, as 16-bit numbers, and the
+// More rows: the states are loaded into the workspace once, as 16-bit numbers, and the
 // cross attention kernel runs on them.
+//
+// What bounds it, measured on MI355Xs: one token for each of 4 entries over 32771 keys, 16
+// query and 2 key heads of 128, bf16: 17.4 us with the joining launch (16-bit states: 30.9),
+// the read 14.4 us of it, 4.7 TB/s; 1024 rows over 4 x 4096 keys, 2 heads of 128: 30.6 us;
+// loaded first, 3600 tokens over 3600, 2 x 8 heads of 64, fp16: 80, of which the load is 5.
 #include <float.h>
 #include <math.h>
 
@@ -313,13 +318,14 @@ bool configure_held(HeldPlan &p) {
   p.rows = d.lq * p.group;
   p.row_tiles = (p.rows + 31) / 32;
   const int64_t blocks = held_blocks(h.len), units = (int64_t)h.n * h.heads * p.row_tiles;
-  // The held bytes directly up to four workgroups a CU's pair of slots (heads over 128: one
-  // slot); beyond, the products take so long that loading the states first for the faster
-  // kernel pays. Direct and loaded: 2 entries x 8 heads of 64 over 3600 keys, 3600 rows (1808
+  // The held bytes directly up to 1024 row tiles (heads over 128: 512); beyond, the products
+  // take so long that loading the states first for the faster kernel pays. Direct and loaded: 2 entries x 8 heads of 64 over 3600 keys, 3600 rows (1808
   // workgroups) 81.8 and 79.8 us, 1024 rows (512) 25.5 and 40.2; 4 x 2 heads of 128 over 4096
   // keys, 4096 rows (1024) 80.8 and 80.2, 8192 rows 160 and 136; 2 heads of 256 over 2000 keys,
   // 8192 rows (512) 58 and 64, 14400 rows 109 and 81.
-  p.direct = units <= (held_padded(h.d) <= 128 ? 1024 : 512);
+  // (A token of more than 2^23 elements is beyond that kernel's strides.)
+  const int64_t token = (int64_t)h.heads * h.d;
+  p.direct = units <= (held_padded(h.d) <= 128 ? 1024 : 512) || token > (int64_t)1 << 23;
   p.splits = 1;
   p.split_blocks = (int)(blocks < 1 ? 1 : blocks);
   p.workgroups = units;
@@ -351,7 +357,7 @@ bool configure_held(HeldPlan &p) {
   }
   AttentionPlan &c = p.loaded;
   c.d = {h.n, d.lq, h.len, d.hq, h.heads, h.d, h.dtype, d.scale, {}, {}, {}, {}, d.mask_batch_stride};
-  const int64_t token = (int64_t)h.heads * h.d, batch = token * h.len;
+  const int64_t batch = token * h.len;
   for (int i = 0; i < 3; ++i) {
     c.d.q_stride[i] = d.q_stride[i];
     c.d.out_stride[i] = d.out_stride[i];
@@ -359,7 +365,6 @@ bool configure_held(HeldPlan &p) {
   }
   c.scale = p.scale;
   p.name = "is_k14_held_load, is_k11_attention";
-  if (token > (int64_t)1 << 23) return false;
   return configure_attention(c);
 }
 

@@ -2,9 +2,10 @@
  * imgstencil.h -- C ABI of the MI355X (gfx950) direct 2D convolution library.
  *
  * The operation (the conv2d_* and conv_chain_* entry points compute it, or a
- * chain of it; the attention operators for networks that put attention between
- * their convolution layers are the rotary_*, qk_norm_rotary_* and
- * cross_attention_* entry points at the end, with their own conventions there):
+ * chain of it; the operators for networks that put attention between their
+ * convolution layers are the rotary_*, qk_norm_rotary_*, cross_attention_*,
+ * block_norm_*, dense_* and held_* entry points at the end, with their own
+ * conventions there):
  *
  *   y[n,k,i,j] = act( sum_{c,u,v} w[k,c,u,v] * x[n,c,i+u-(R-1)/2,j+v-(S-1)/2] + b[k] )
  *
@@ -65,7 +66,7 @@ typedef enum {
 typedef enum {
   IS_F32 = 0,
   IS_F16 = 1,
-  IS_BF16 = 2               /* attention operators only: the convolutions answer IS_ERR_UNSUPPORTED */
+  IS_BF16 = 2               /* the operators at the end only: the convolutions answer IS_ERR_UNSUPPORTED */
 } is_dtype;
 typedef enum { IS_NCHW = 0, IS_NHWC = 1 } is_layout;
 
@@ -502,8 +503,8 @@ typedef struct {
  *                apart (0: one row for all), or NULL for ones (gate) and zeros
  *  post_weight, weight, bias: c fp32 values or NULL (ones; bias: zeros)
  *  eps         : >= 0, finite; residual_scale: finite
- * x_out and out may each be x or y itself with the same strides; otherwise
- * outputs overlap nothing (IS_ERR_INVALID_ARG). Rows may start at any element;
+ * x_out and out may each be x or y itself with the same strides; otherwise the
+ * address range of an output meets no other range (IS_ERR_INVALID_ARG). Rows may start at any element;
  * bases are 16-byte aligned, those of the vectors aligned to their type. Errors: also IS_ERR_UNSUPPORTED (c over IS_MAX_NORM_CHANNELS, dtype,
  * sizes that need 2^32 or more threads). */
 typedef struct {
@@ -531,7 +532,8 @@ is_status block_norm_forward(const block_norm_desc *d, const void *x, const void
  *               apart; strides multiples of 8 (IS_ERR_MISALIGNED), row strides at
  *               most 2^21
  *  residual   : n x len rows of `features` or absent (at forward: NULL), with
- *               strides of its own; it may be out itself with the same strides
+ *               strides of its own (zeros if there is none); it may be out itself
+ *               with the same strides
  *  bias       : `features` fp32 values or NULL
  * Sums are fp32; bias, activation and residual are applied to the sum in fp32 and
  * the result is rounded once. */

@@ -88,6 +88,12 @@ def test_block_norm_calls_fit_a_launch():
     st = _abi.load().block_norm_forward(ctypes.byref(d), far, 2 * far, None, None, None, None, None, None, 3 * far, 4 * far,
                                         None)
     assert st == UNSUPPORTED
+    # more rows than 32 bits count, in few channels
+    r = _abi.is_rows(2 ** 30, 2 ** 12, 2 ** 12, 1)
+    d = _abi.block_norm_desc(_abi.IS_F16, 1, 1, 0, 1e-6, 1.0, r, r, r, r, 0, 0, 0)
+    st = _abi.load().block_norm_forward(ctypes.byref(d), 1 << 44, None, None, None, None, None, None, None, None, 1 << 45,
+                                        None)
+    assert st == UNSUPPORTED
 
 
 # ------------------------------------------------------------------- dense, C ABI
@@ -153,6 +159,50 @@ def test_dense_forward_refusals():
     _, plan = _dense(n=0)
     assert lib.dense_forward(plan, None, None, None, None, None, None, 0, None) == 0
     lib.dense_destroy(plan)
+
+
+@pytest.mark.parametrize("n,length,k,m", [(1, 1, 8, 1), (1, 1, 16384, 8192), (1, 40, 8192, 64), (16, 1, 1024, 4096),
+                                          (3, 1021, 344, 777), (1, 2 ** 20, 64, 64), (2 ** 20, 1, 64, 64), (1, 256, 64, 8192),
+                                          (1, 257, 8, 9), (5, 100, 4096, 1024)])
+@pytest.mark.parametrize("gap", [0, 8])
+def test_dense_plans_cover_their_rows_and_features(n, length, k, m, gap):
+    """Tiles times their number hold all rows and features, and a split sum's workspace
+    every part; entries with gaps between them are not joined."""
+    batch = length * k + gap
+    st, plan = _dense(n=n, length=length, k=k, m=m, xs=(batch, k))
+    assert st == 0
+    info, ws = _abi.conv2d_plan_info(), ctypes.c_size_t()
+    lib = _abi.load()
+    assert lib.dense_get_plan_info(plan, ctypes.byref(info)) == 0
+    assert lib.dense_workspace_size(plan, ctypes.byref(ws)) == 0
+    one = gap == 0 or n == 1 or length == 1
+    entries, rows = (1, n * length) if one else (n, length)
+    tiles = entries * -(-rows // info.tile_h) * -(-m // info.tile_w)
+    assert info.grid_x == tiles and info.flops == 2.0 * n * length * k * m
+    assert ws.value == (0 if info.grid_y == 1 else info.grid_y * n * length * -(-m // 8) * 8 * 4)
+    assert 1 <= info.grid_y <= max(1, -(-k // 64))
+    lib.dense_destroy(plan)
+
+
+@pytest.mark.parametrize("lq,length,hq,heads,d", [(1, 1, 1, 1, 8), (1, 40000, 8, 1, 128), (5, 100, 4, 2, 40), (1000, 333, 4, 4, 64),
+                                                  (9000, 300, 8, 8, 64), (40, 0, 2, 1, 256), (300, 9000, 16, 4, 256)])
+def test_held_attention_plans_cover_their_keys_and_rows(lq, length, hq, heads, d):
+    n = 2
+    st, plan = _attend(n=n, length=length, heads=heads, d=d, lq=lq, hq=hq, mb=length)
+    assert st == 0
+    info, ws = _abi.conv2d_plan_info(), ctypes.c_size_t()
+    lib = _abi.load()
+    assert lib.held_attention_get_plan_info(plan, ctypes.byref(info)) == 0
+    assert lib.held_attention_workspace_size(plan, ctypes.byref(ws)) == 0
+    rows = lq * (hq // heads)
+    assert info.grid_y * info.tile_w >= length
+    if info.kernel == b"is_k15_held_attention":
+        assert info.tile_w % 32 == 0 and (info.grid_y - 1) * info.tile_w < max(length, 1)
+        assert info.grid_x == n * heads * -(-rows // 32)
+        assert ws.value == (0 if info.grid_y == 1 else info.grid_x * info.grid_y * 32 * (d + 1) * 4)
+    else:
+        assert rows > 32 and ws.value >= 2 * n * length * heads * d * 2
+    lib.held_attention_destroy(plan)
 
 
 def test_dense_split_plans_need_their_workspace():
