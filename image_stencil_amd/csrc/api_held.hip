@@ -156,7 +156,7 @@ is_status held_load(const held_states_desc *d, const void *held, size_t held_siz
   const Range rk = range(k, *kt, d->d, 2), rv = range(v, *vt, d->d, 2), from = store_range(*d, held);
   // Slices of one packed buffer lie between each other; that they are apart is the caller's.
   if (intersect(rk, from) || intersect(rv, from) || collide(k, *kt, v, *vt, d->d, 2)) return IS_ERR_INVALID_ARG;
-  return is::report_hip(is::launch_held_load(*d, held, at, kt->len, side(*kt, k), side(*vt, v), stream));
+  return is::report_hip(is::launch_held_load(*d, held, at, kt->len, side(*kt, k), side(*vt, v), false, stream));
 }
 
 is_status held_attention_create(const held_attention_desc *d, held_attention_plan *out) {

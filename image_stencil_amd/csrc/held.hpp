@@ -33,7 +33,7 @@ hipError_t launch_held_store(const held_states_desc &d, const HeldSide &k, const
                              const uint8_t *mask, int64_t mask_stride, const int32_t *lengths, void *held,
                              hipStream_t s);
 hipError_t launch_held_load(const held_states_desc &d, const void *held, int at, int len, const HeldSide &k,
-                            const HeldSide &v, hipStream_t s);
+                            const HeldSide &v, bool read_next, hipStream_t s);
 
 struct HeldPlan {
   held_attention_desc d;

@@ -17,11 +17,12 @@
 // Bound: one read and one write of every element. 8 x 16384 rows of 1024 bf16 channels
 // with both norms and all vectors: 212 us, 5.07 TB/s, the rate of a large copy (213); two
 // frames of 3600 rows of 512 fp16 channels: 9.3 us; 3063 rows of 1001 fp32 channels: 13.7
-// (floor 9.8 and a launch); one row: 5.1 in a graph.
+// (floor 9.8 and a launch); one row: 4.0 in a graph.
 #include <math.h>
 
 #include "blocks.hpp"
 #include "common.hpp"
+#include "divide.hpp"
 
 namespace is {
 namespace {
@@ -32,6 +33,7 @@ struct Args {
   int entries, len, c, groups;   // groups of threads that share an entry's rows
   int norm, post;
   float eps, alpha, inv_c;
+  Divisor by_groups;
 };
 
 // Threads of a workgroup: one row where waves share it (they meet at barriers), else
@@ -67,9 +69,9 @@ __global__ __launch_bounds__(block_of(TPR)) void is_k12_block_norm(const Args a)
   lds_poison(shared, sizeof(shared));
   int turn = 0;
   const int lane = threadIdx.x % TPR;
-  const int64_t g = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
-  const int b = (int)(g / a.groups);
-  int i = (int)(g - (int64_t)b * a.groups);
+  const unsigned g = blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;      // under 2^32 threads / 16
+  const int b = divide((int)g, a.by_groups);
+  int i = (int)g - b * a.groups;
   if (b >= a.entries) return;     // whole groups of threads leave
 
   // Vector v of a thread: elements at .. at + V - 1, the last one cut at c.
@@ -291,6 +293,7 @@ hipError_t launch_block_norm(const block_norm_desc &d, const NormPointers &p, hi
   a.len = d.x.len;
   a.c = d.c;
   a.groups = groups_of(d);
+  a.by_groups = divisor((unsigned)a.groups);
   a.norm = d.norm;
   a.post = d.post;
   a.eps = d.eps;

@@ -11,9 +11,9 @@
 // leaves in whole lines.
 //
 // Bound: one read of the states and one write of half their bytes, and back. 4 entries of
-// 16384 tokens, 4 heads of 128, bf16, put and got: 93 us, 4.3 TB/s (a copy's rate: 80), of
-// which the load 40 (5.0 TB/s) and the store about 50: its workgroups, of 24 KB each,
-// load, reduce and store in turn. (Single bytes to LDS in place of words of four tokens: 57.)
+// 16384 tokens, 4 heads of 128, bf16: put 44.8 us, got 37.3, 81 together, the rate of a large
+// copy (80). What is read or written once passes the caches by: 52 and 48.6 us without
+// that. (Single bytes to LDS in place of words of four tokens: put 57.)
 #include <math.h>
 
 #include "common.hpp"
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads) void is_k14_held_store(const Args a) {
     const int at = blk * 32 + token;
     bool in = e < a.d && at < len;
     if (in && a.mask) in = a.mask[b * a.mask_stride + at] != 0;
-    return in ? *reinterpret_cast<const uvec *>(p + at * t.token + e) : uvec{};
+    return in ? __builtin_nontemporal_load(reinterpret_cast<const uvec *>(p + at * t.token + e)) : uvec{};
   };
   // Key vector i: token item / CH. Value four i: tokens 8 a + 4 half + (0..3) of group 2 a + half.
   uvec x[NV];
@@ -167,7 +167,8 @@ __global__ __launch_bounds__(kThreads) void is_k14_held_store(const Args a) {
   if (thread == 0) *reinterpret_cast<float *>(a.held + a.scales_at + (rec * 2 + side) * 4) = scale;
 }
 
-template <typename T, int DP>
+// READ_NEXT: by the next kernel, so that the caches are to keep it.
+template <typename T, int DP, bool READ_NEXT>
 __global__ __launch_bounds__(kThreads) void is_k14_held_load(const Args a) {
   typedef T uvec __attribute__((ext_vector_type(8), aligned(sizeof(T))));
   typedef float F2 __attribute__((ext_vector_type(2)));
@@ -207,7 +208,9 @@ __global__ __launch_bounds__(kThreads) void is_k14_held_load(const Args a) {
         y[4 * j + 2] = (T)(hi[0] * scale);
         y[4 * j + 3] = (T)(hi[1] * scale);
       }
-      *reinterpret_cast<uvec *>(p + at * t.token + e) = y;
+      uvec *to = reinterpret_cast<uvec *>(p + at * t.token + e);
+      if constexpr (READ_NEXT) *to = y;
+      else __builtin_nontemporal_store(y, to);
     }
   }
 }
@@ -259,13 +262,14 @@ hipError_t launch_held_store(const held_states_desc &d, const HeldSide &k, const
 }
 
 hipError_t launch_held_load(const held_states_desc &d, const void *held, int at, int len, const HeldSide &k,
-                            const HeldSide &v, hipStream_t s) {
+                            const HeldSide &v, bool read_next, hipStream_t s) {
   const Args a = arguments_of(d, k, v, len, at, held);
   const dim3 grid((unsigned)((int64_t)d.n * d.heads * a.blocks));
   return for_padded(held_padded(d.d), [&](auto dp) {
     constexpr int DP = decltype(dp)::value;
-    return d.dtype == IS_F16 ? launch_kernel(is_k14_held_load<_Float16, DP>, grid, dim3(kThreads), 0, s, a)
-                             : launch_kernel(is_k14_held_load<__bf16, DP>, grid, dim3(kThreads), 0, s, a);
+    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, a); };
+    if (d.dtype == IS_F16) return read_next ? go(is_k14_held_load<_Float16, DP, true>) : go(is_k14_held_load<_Float16, DP, false>);
+    return read_next ? go(is_k14_held_load<__bf16, DP, true>) : go(is_k14_held_load<__bf16, DP, false>);
   });
 }
 

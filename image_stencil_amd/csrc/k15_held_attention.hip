@@ -381,7 +381,7 @@ hipError_t launch_held_attention(const HeldPlan &p, const void *q, const void *h
     char *k = static_cast<char *>(ws), *v = k + loaded_bytes(p), *more = v + loaded_bytes(p);
     const int64_t token = (int64_t)h.heads * h.d, batch = token * h.len;
     if (h.n > 0 && h.len > 0) {
-      const hipError_t e = launch_held_load(h, held, 0, h.len, {k, batch, token, h.d}, {v, batch, token, h.d}, s);
+      const hipError_t e = launch_held_load(h, held, 0, h.len, {k, batch, token, h.d}, {v, batch, token, h.d}, true, s);
       if (e != hipSuccess) return e;
     }
     return launch_attention(p.loaded, q, k, v, mask, lengths, out, lse, more, s);
