@@ -211,6 +211,8 @@ class Dense:
         if k > 1 and w.stride(1) != 1:
             raise ValueError("w must have a contiguous last dimension")
         m = w.shape[0]
+        if m > _INT_MAX:
+            raise ValueError("w has a dimension over %d, got shape %s" % (_INT_MAX, tuple(w.shape)))
         shape = torch.Size((n, length, m))
         dense = (length * m, m, 1)
         for name, t in (("out", out), ("residual", residual)):
