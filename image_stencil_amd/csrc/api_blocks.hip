@@ -85,11 +85,16 @@ is_status run_norm(const block_norm_desc &d, const is::NormPointers &p, hipStrea
   return is::report_hip(is::launch_block_norm(d, p, stream));
 }
 
+constexpr int kMaxSize = 2147483000;
+
 is_status check_dense(const dense_desc *d) {
   if (!d) return IS_ERR_INVALID_ARG;
   if (d->n < 0 || d->len < 0 || d->in < 1 || d->features < 1) return IS_ERR_INVALID_ARG;
   if (d->activation < IS_ACT_NONE || d->activation > IS_ACT_SILU || d->w_stride < 0) return IS_ERR_INVALID_ARG;
   if ((d->dtype != IS_F16 && d->dtype != IS_BF16) || d->in % 8) return IS_ERR_UNSUPPORTED;
+  // Rounded up to whole tiles they are still ints.
+  for (const int size : {d->len, d->in, d->features})
+    if (size > kMaxSize) return IS_ERR_UNSUPPORTED;
   const is_tokens tx = rows(d->n, d->len, d->x_stride), tr = rows(d->n, d->len, d->residual_stride),
                   to = rows(d->n, d->len, d->out_stride);
   is_status st = check_tokens(tx, d->in, 2);

@@ -504,8 +504,9 @@ typedef struct {
  *  post_weight, weight, bias: c fp32 values or NULL (ones; bias: zeros)
  *  eps         : >= 0, finite; residual_scale: finite
  * x_out and out may each be x or y itself with the same strides; otherwise the
- * address range of an output meets no other range (IS_ERR_INVALID_ARG). Rows may start at any element;
- * bases are 16-byte aligned, those of the vectors aligned to their type. Errors: also IS_ERR_UNSUPPORTED (c over IS_MAX_NORM_CHANNELS, dtype,
+ * address range of an output meets no other range (IS_ERR_INVALID_ARG). Rows may
+ * start at any element; bases are 16-byte aligned, those of the vectors aligned to
+ * their type. Errors: also IS_ERR_UNSUPPORTED (c over IS_MAX_NORM_CHANNELS, dtype,
  * sizes that need 2^32 or more threads). */
 typedef struct {
   is_dtype dtype;
@@ -526,7 +527,7 @@ is_status block_norm_forward(const block_norm_desc *d, const void *x, const void
  * IS_ACT_GELU_TANH its form with tanh(sqrt(2/pi) (x + 0.044715 x^3)), IS_ACT_SILU
  * is x / (1 + exp(-x)). At -infinity these three give their limit, zero.
  *  in, features: k inputs, a multiple of 8 (IS_ERR_UNSUPPORTED), and any number
- *               of outputs, both >= 1
+ *               of outputs, both >= 1 and, like len, at most 2147483000
  *  dtype      : IS_F16 or IS_BF16 of x, w, residual and out
  *  x          : n x len rows of `in`, w: `features` rows of `in`, w_stride elements
  *               apart; strides multiples of 8 (IS_ERR_MISALIGNED), row strides at

@@ -126,6 +126,14 @@ def test_dense_create_refusals(kw, status):
     _abi.load().dense_destroy(plan)
 
 
+@pytest.mark.parametrize("kw", [dict(n=1, length=2 ** 31 - 1, k=8, m=8), dict(n=1, length=1, k=2 ** 31 - 8, m=1),
+                                dict(n=1, length=1, k=8, m=2 ** 31 - 1), dict(n=2, length=2 ** 31 - 64, k=8, m=8)])
+def test_dense_sizes_that_whole_tiles_take_past_an_int(kw):
+    """Rows, inputs or features rounded up to tiles would be negative."""
+    st, plan = _dense(xs=(0, 0), os=(2 ** 31 * 8, 8), rs=(0, 0), **kw)
+    assert st == UNSUPPORTED and not plan.value
+
+
 def test_dense_null_arguments():
     lib, n, info = _abi.load(), ctypes.c_size_t(), _abi.conv2d_plan_info()
     d = _dense_desc()
