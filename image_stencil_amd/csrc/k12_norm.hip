@@ -71,7 +71,7 @@ __global__ __launch_bounds__(block_of(TPR)) void is_k12_block_norm(const Args a)
   const int lane = threadIdx.x % TPR;
   const unsigned g = blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;      // under 2^32 threads / 16
   const int b = divide((int)g, a.by_groups);
-  int i = (int)g - b * a.groups;
+  unsigned i = g - (unsigned)(b * a.groups);      // past the last row it may pass 2^31
   if (b >= a.entries) return;     // whole groups of threads leave
 
   // Vector v of a thread: elements at .. at + V - 1, the last one cut at c.
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(block_of(TPR)) void is_k12_block_norm(const Args a)
   T *out = static_cast<T *>(a.p.out) + b * a.ob;
   const bool has_y = a.p.y != nullptr;
   vec rx[NV] = {}, ry[NV] = {};
-  auto fetch = [&](int row) {
+  auto fetch = [&](unsigned row) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       rx[v] = load(x + row * a.xr, v);
@@ -187,9 +187,9 @@ __global__ __launch_bounds__(block_of(TPR)) void is_k12_block_norm(const Args a)
         f[v][j] = (float)rx[v][j];
         h[v][j] = (float)ry[v][j];
       }
-    const int row = i;
+    const unsigned row = i;
     i += a.groups;
-    if (E <= 16 && i < a.len) fetch(i);     // (32 elements leave no registers for more)
+    if (E <= 16 && i < (unsigned)a.len) fetch(i);     // (32 elements leave no registers for more)
     if (has_y) {
       if (a.post) normed(h, a.post);
 #pragma unroll
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(block_of(TPR)) void is_k12_block_norm(const Args a)
         store(out + row * a.orow, v, f[v]);
       }
     }
-    if (i >= a.len) break;
+    if (i >= (unsigned)a.len) break;
     if constexpr (E > 16) fetch(i);
   }
 }

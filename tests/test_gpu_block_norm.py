@@ -177,3 +177,12 @@ def test_in_a_graph_and_on_streams():
     plan.apply(buf, x_out=outs[0], out=outs[1], stream=side.cuda_stream, **dev)
     side.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_as_many_rows_as_an_int_counts():
+    """The last step of a walk over the rows of an entry passes 2^31."""
+    rows = 2 ** 31 - 1
+    x = torch.full((1, 1, 1), 2.0, dtype=torch.bfloat16, device="cuda").expand(1, rows, 1)
+    _, out = isa.BlockNorm(1, eps=12.0).apply(x)      # 2 / sqrt(4 + 12)
+    assert out.shape == x.shape
+    assert all(bool((part == 0.5).all()) for part in out.view(-1).split(1 << 28))
