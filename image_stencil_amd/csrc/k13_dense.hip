@@ -22,11 +22,13 @@
 // rows, 4096 to 1024, with residual: 448 to 468 us, 1.17 to 1.23 PFLOP/s; 8192 cubed 809
 // to 841, 1.31 to 1.36 PFLOP/s: matrix cores 77% busy at 1.4 to 1.7 GHz, which the power
 // limit sets (a library product without residual: 377 and 690). Two 3600-token frames, 512
-// to 2048, GELU: 27.3 to 28.5; 8 steps are 12.4 of it, the activations and the write of a
-// whole tile per CU most of the rest. 16 rows, 8192 to 8192: 33, 4.1 TB/s (one row 28): the
+// to 2048: 22.9 us without an activation, 23.2 ReLU, 26.2 SiLU, 26.7 tanh-GELU, 29.0 GELU (an
+// end that knows of no residual and shorter activations: 23.5, 24.1, 26.4, 27.3, 30.5 before);
+// 8 steps are 12.4 of it, the write of a whole tile per CU much of the rest. 16 rows, 8192 to 8192: 33, 4.1 TB/s (one row 28): the
 // 16 rows of x, read again by each workgroup, are as many requests as half the weights.
 // Steps that were taken back: touching the lines of later steps (a dword of each, 892 to
-// 1050); both quarters of an accumulator's half step one after the other (841 to 874).
+// 1050); both quarters of an accumulator's half step one after the other (841 to 874); weights
+// of few rows past the caches (33.6 to 35.9: an instruction takes half of each line).
 #include <math.h>
 
 #include "blocks.hpp"
@@ -68,34 +70,34 @@ __device__ __forceinline__ floatx4 mma16(bfx8 a, bfx8 b, floatx4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+// x / (1 + 2^u). Where the exponential overflows, the quotient is zero: x is kept finite
+// for the product.
+__device__ __forceinline__ float over(float x, float u) {
+  return fmaxf(x, -3.4e38f) * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u));
 }
 
 // GELU is x Phi(x) = max(x, 0) - |x| Phi(-|x|), with Phi(-z) = exp(-z^2 / 2) R(z) and R a
 // polynomial in t = 1 / (1 + 0.31 z), fitted to erfcx(z / sqrt 2) / 2 on 0 <= z <= 14:
 // within 4.7e-6 of it everywhere, a hundredth of fp16's half step, so that small
-// results at far negative x keep their digits. Where an exponential overflows, the
-// factor beside it is zero: x is kept finite for that product.
+// results at far negative x keep their digits. NaN stays NaN in all. (Every instruction
+// counts: for the 65536 results of a CU's tile one takes 0.4 us.)
 template <int ACT>
 __device__ __forceinline__ float activated(float x) {
-  if constexpr (ACT == IS_ACT_RELU) return x < 0.f ? 0.f : x;     // NaN stays
+  if constexpr (ACT == IS_ACT_RELU) return __builtin_elementwise_maximum(x, 0.f);
   if constexpr (ACT == IS_ACT_GELU) {
-    const float z = fminf(fabsf(x), 14.f), t = __builtin_amdgcn_rcpf(1.f + 0.31f * z);
+    const float z = __builtin_elementwise_minimum(fabsf(x), 14.f), t = __builtin_amdgcn_rcpf(1.f + 0.31f * z);
     float r = -0.07392936f;
     r = r * t + 0.18045098f;
     r = r * t + 0.01574401f;
     r = r * t + 0.13343013f;
     r = r * t + 0.1204412f;
     r = r * t + 0.12386071f;
-    const float tail = z * t * r * __builtin_amdgcn_exp2f(-0.72134752f * z * z);
-    return (x < 0.f ? 0.f : x) - tail;
+    return fmaxf(x, 0.f) - z * (t * r * __builtin_amdgcn_exp2f(-0.72134752f * z * z));
   }
-  if constexpr (ACT == IS_ACT_GELU_TANH) {
-    const float u = 1.5957691216f * (x + 0.044715f * x * x * x);    // 2 sqrt(2 / pi)
-    return fmaxf(x, -3.4e38f) * sigmoid(u);
+  if constexpr (ACT == IS_ACT_GELU_TANH) {      // x / (1 + exp(-2 sqrt(2 / pi) (x + 0.044715 x^3)))
+    return over(x, x * (-0.10294324f * (x * x) - 2.3022082f));
   }
-  if constexpr (ACT == IS_ACT_SILU) return fmaxf(x, -3.4e38f) * sigmoid(x);
+  if constexpr (ACT == IS_ACT_SILU) return over(x, -1.4426950408889634f * x);
   return x;
 }
 // Calls f(std::integral_constant<int, activation>{}).
@@ -308,12 +310,13 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
   // The residual of 32 tokens is asked for at once, and that of the next 32 before the
   // stores of these, since loads wait for the stores before them. The bias is one value
   // a lane, and reaches the lanes that need it by permutes.
-  auto finish = [&](const Place &p, char *mine, auto kind) {
+  auto finish = [&](const Place &p, char *mine, auto kind, auto with_residual) {
     constexpr int ACT = decltype(kind)::value;
+    constexpr bool RES = decltype(with_residual)::value;
     typedef T uvec __attribute__((ext_vector_type(8), aligned(sizeof(T))));   // at any element
     const int l = fresh_lane(), col = l & 3;
     const int f = p.ft * G::TF + wf * 32 * FB, row0 = p.rt * G::TT + wt * 32 * TB + (l >> 2);
-    const T *res = a.residual ? static_cast<const T *>(a.residual) + p.entry * a.rb + f + col * 8 : nullptr;
+    const T *res = static_cast<const T *>(a.residual) + p.entry * a.rb + f + col * 8;
     T *out = static_cast<T *>(a.out) + p.entry * a.ob + f + col * 8;
     const int left = a.features - f - col * 8;        // features from this lane's first on
     float bias[(FB + 1) / 2];
@@ -329,7 +332,7 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
         const int row = row0 + j * 32 + 16 * (u & 1);
         T8 &x = r[j & 1][I][u & 1];
         x = T8{};
-        if (!res || row >= a.len) return;
+        if (row >= a.len) return;
         const T *at = res + row * a.rr + I * 32;
         if (left >= I * 32 + 8) {
           x = *reinterpret_cast<const uvec *>(at);
@@ -340,7 +343,7 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
         }
       });
     };
-    ask_residual(std::integral_constant<int, 0>{});
+    if constexpr (RES) ask_residual(std::integral_constant<int, 0>{});
     static_for<TB>([&](auto j) {
       static_for<FB>([&](auto i) {
         float b[8];
@@ -355,7 +358,10 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
           unstage(s, mine, z, l);
           T8 &x = r[j & 1][i][s];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = (T)((float)x[e] + activated<ACT>(z[e] + b[e]));
+          for (int e = 0; e < 8; ++e) {
+            const float y = activated<ACT>(z[e] + b[e]);
+            x[e] = (T)(RES ? (float)x[e] + y : y);
+          }
           // Computed here, not beside its store, up to which every sum would be kept.
           uintx4 bits = __builtin_bit_cast(uintx4, x);
           __asm__ volatile("" : "+v"(bits));
@@ -363,7 +369,7 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
         });
         __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (j + 1 < TB) ask_residual(std::integral_constant<int, j + 1>{});
+      if constexpr (RES && j + 1 < TB) ask_residual(std::integral_constant<int, j + 1>{});
       static_for<2 * FB>([&](auto u) {
         constexpr int I = decltype(u)::value >> 1;
         const int row = row0 + j * 32 + 16 * (u & 1);
@@ -452,7 +458,8 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
     if (free >= G::SLOTS * G::SLOT) free -= G::SLOTS * G::SLOT;
     char *mine = lds + free + wave * NI * 1024;
     if (a.splits > 1) finish_part(p, mine);
-    else for_activation(a.act, [&](auto kind) { finish(p, mine, kind); });
+    else if (a.residual) for_activation(a.act, [&](auto kind) { finish(p, mine, kind, std::true_type{}); });
+    else for_activation(a.act, [&](auto kind) { finish(p, mine, kind, std::false_type{}); });
     // Again (the registers were needed meanwhile).
     static_for<OPERANDS>([&](auto o) { read(ws, xs, 0, o); });
   }
