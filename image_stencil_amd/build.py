@@ -8,6 +8,7 @@ import glob
 import os
 import subprocess
 import sys
+import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,8 +57,7 @@ def _build_probes(verbose):
 def _compile_and_link(variants, verbose, jobs):
     """Compile every csrc/*.hip of every variant to objects in parallel, then
     link each variant's library."""
-    procs, objs = [], {}
-    running = []
+    procs, objs, todo = [], {}, []
     for lib, objname, defines in variants:
         objdir = os.path.join(HERE, objname)
         os.makedirs(objdir, exist_ok=True)
@@ -65,15 +65,19 @@ def _compile_and_link(variants, verbose, jobs):
         for src in sources():
             obj = os.path.join(objdir, os.path.basename(src) + ".o")
             objs[lib].append(obj)
-            cmd = [HIPCC] + FLAGS + defines + ["-c", src, "-o", obj]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            p = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-            procs.append((src, p))
-            running.append(p)
-            while len([q for q in running if q.poll() is None]) >= jobs:
-                running[0].wait()
-                running = [q for q in running if q.poll() is None]
+            todo.append((src, [HIPCC] + FLAGS + defines + ["-c", src, "-o", obj]))
+    # The long ones first, and the next as soon as any ends: a few take minutes each.
+    todo.sort(key=lambda job: -os.path.getsize(job[0]))
+    running = []
+    for src, cmd in todo:
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        p = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        procs.append((src, p))
+        running.append(p)
+        while len(running) >= jobs:
+            time.sleep(0.05)
+            running = [q for q in running if q.poll() is None]
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
