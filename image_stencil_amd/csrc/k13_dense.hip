@@ -188,7 +188,7 @@ __global__ __launch_bounds__(WF *WT * 64, 2) void is_k13_dense(const Args a) {
     p.ft = high == 8 ? in_span >> 3 : divide(in_span, a.by_last);
     p.rt = first + in_span - p.ft * high;
     p.in0 = p.split * a.split_in;
-    p.in1 = min(a.in, p.in0 + a.split_in);
+    p.in1 = p.in0 + min(a.in - p.in0, a.split_in);      // (in0 + split_in may pass an int)
     return p;
   };
   auto steps_of = [](const Place &p) { return (p.in1 - p.in0 + 63) / 64; };

@@ -1,0 +1,25 @@
+"""Dense layers at the ends of what a plan takes."""
+import pytest
+import torch
+
+import image_stencil_amd as isa
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+F16 = torch.float16
+
+
+def test_a_sum_of_almost_2_to_the_31_inputs_in_parts():
+    """The last of 16 parts ends before 2^31, where its nominal end does not fit an int. Ones
+    at both ends of every part count each part once; ones behind both rows count nothing."""
+    k, part = 2147483000, 134217728
+    say("dense inputs", k)
+    x, w = (torch.zeros(k + 1024, dtype=F16, device="cuda") for _ in range(2))
+    for t in (x, w):
+        t[k:] = 1.0
+        for at in range(0, k, part):
+            t[at], t[at + 63], t[min(k, at + part) - 1] = 1.0, 1.0, 1.0
+    xs, ws = x[:k].view(1, 1, k), w[:k].view(1, k)
+    plan = isa.Dense(xs, ws)
+    assert plan.info()["grid"] == (1, 16, 1) and plan.info()["kernel"] == "is_k13_dense"
+    assert plan.forward(xs, ws).item() == 48.0
