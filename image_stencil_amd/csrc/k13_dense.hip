@@ -594,6 +594,7 @@ struct FewShape {
 constexpr FewShape kFew[] = {{1, 1}, {2, 1}, {2, 2}};
 constexpr int kFewWaves = 8;
 constexpr int kFewMost = 256;     // rows up to which they are looked at
+constexpr double kMaxUnits = 2147483000.0;    // tiles of a call, counted in an int
 
 // Workgroups for `units` tiles: as many as the device holds at a time, and a multiple
 // of 8 (an XCD each). A workgroup without a tile leaves at once.
@@ -690,10 +691,15 @@ bool configure_dense(DensePlan &p) {
     if (better) best = us;
     return better;
   };
+  // Tiles of a call: a form that cannot be launched with so many is passed over.
+  auto tiles = [&](int rows, int features) {
+    return (double)d.n * ceil((double)d.len / rows) * ceil((double)d.features / features);
+  };
   for (int i = 0; i < 3; ++i)
     for (int64_t n = 1; n <= 16 && n <= steps; n *= 2) {
       const int64_t per = (steps + n - 1) / n, parts = (steps + per - 1) / per;
       if (parts != n && n > 1) continue;
+      if (tiles(kTiles[i].rows, kTiles[i].features) * parts > kMaxUnits) continue;
       const double join = (double)d.n * d.len * ((d.features + 7) / 8);      // its threads
       if (n > 1 && join > kMaxLaunchThreads - 256) continue;
       if (!take(tile_us(d, i, (int)parts))) continue;
@@ -703,12 +709,14 @@ bool configure_dense(DensePlan &p) {
       p.split_in = (int)per * 64;
     }
   for (int i = 0; i < 3 && d.len <= kFewMost; ++i) {
+    if (tiles(16 * kFew[i].rows, 16 * kFew[i].features) * 64 * kFewWaves > kMaxLaunchThreads) continue;
     if (!take(few_us(d, i))) continue;
     p.few = true;
     p.tile = i;
     p.splits = 1;
     p.split_in = (int)steps * 64;
   }
+  if (best == 0.0) return false;      // no form can be launched
   if (p.few) {
     p.tile_rows = 16 * kFew[p.tile].rows;
     p.tile_features = 16 * kFew[p.tile].features;
@@ -724,8 +732,7 @@ bool configure_dense(DensePlan &p) {
   }
   p.row_tiles = (d.len + p.tile_rows - 1) / p.tile_rows;
   p.feature_tiles = (d.features + p.tile_features - 1) / p.tile_features;
-  const double units = (double)d.n * p.row_tiles * p.feature_tiles * p.splits;
-  return p.few ? units * p.block <= kMaxLaunchThreads : units <= 2147483000.0;
+  return true;
 }
 
 size_t dense_workspace(const DensePlan &p) {
