@@ -85,7 +85,9 @@ def _check_keys(n, length, key_mask, key_lengths):
 class HeldStates:
     """Keys and values of n entries, up to `length` tokens and `heads` key heads of d
     elements (a multiple of 8), held in 8 bits on `device`; zeros at first. dtype
-    (float16 or bfloat16) is that of the tensors put in and got out and of the queries."""
+    (float16 or bfloat16) is that of the tensors put in and got out and of the queries.
+    The constructor waits until the zeros are there, so that any stream may use the
+    store; made while torch's current stream is captured, it is cleared by the graph."""
 
     def __init__(self, n, length, heads, d, dtype=None, device="cuda"):
         import torch
@@ -100,6 +102,10 @@ class HeldStates:
         self.desc = held_states_desc(n, length, heads, d, codes[dtype])
         self.bytes = held_states_size(self.desc)
         self.data = torch.zeros(self.bytes, dtype=torch.uint8, device=device)
+        if self.data.is_cuda:
+            with torch.cuda.device(self.data.get_device()):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
         self._ref = ctypes.byref(self.desc)
         self._lib, self._layouts = _abi.load(), _Layouts()
         self._current_device, self._current_stream = _device_calls()
