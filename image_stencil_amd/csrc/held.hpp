@@ -12,6 +12,8 @@
 // of k and v of each, two floats.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.hpp"
 #include "imgstencil.h"
 
@@ -22,6 +24,21 @@ inline int64_t held_blocks(int len) { return ((int64_t)len + IS_HELD_BLOCK - 1) 
 inline int64_t held_records(const held_states_desc &d) { return (int64_t)d.n * d.heads * held_blocks(d.len); }
 inline int64_t held_scales_at(const held_states_desc &d) { return held_records(d) * 64 * held_padded(d.d); }
 inline size_t held_bytes(const held_states_desc &d) { return (size_t)(held_scales_at(d) + held_records(d) * 8); }
+
+// Calls f(std::integral_constant<int, DP>) for a padded head size.
+template <typename F>
+hipError_t for_padded(int dp, F &&f) {
+  switch (dp) {
+    case 32: return f(std::integral_constant<int, 32>{});
+    case 64: return f(std::integral_constant<int, 64>{});
+    case 96: return f(std::integral_constant<int, 96>{});
+    case 128: return f(std::integral_constant<int, 128>{});
+    case 160: return f(std::integral_constant<int, 160>{});
+    case 192: return f(std::integral_constant<int, 192>{});
+    case 224: return f(std::integral_constant<int, 224>{});
+    default: return f(std::integral_constant<int, 256>{});
+  }
+}
 
 // One side (keys or values) of a store or load: the caller's tensor.
 struct HeldSide {

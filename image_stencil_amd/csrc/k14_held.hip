@@ -215,20 +215,6 @@ __global__ __launch_bounds__(kThreads) void is_k14_held_load(const Args a) {
   }
 }
 
-template <typename F>
-hipError_t for_padded(int dp, F &&f) {
-  switch (dp) {
-    case 32: return f(std::integral_constant<int, 32>{});
-    case 64: return f(std::integral_constant<int, 64>{});
-    case 96: return f(std::integral_constant<int, 96>{});
-    case 128: return f(std::integral_constant<int, 128>{});
-    case 160: return f(std::integral_constant<int, 160>{});
-    case 192: return f(std::integral_constant<int, 192>{});
-    case 224: return f(std::integral_constant<int, 224>{});
-    default: return f(std::integral_constant<int, 256>{});
-  }
-}
-
 Args arguments_of(const held_states_desc &d, const HeldSide &k, const HeldSide &v, int len, int at, const void *held) {
   Args a = {};
   a.side[0] = k;

@@ -274,20 +274,6 @@ __global__ __launch_bounds__(kWaves * 64, Geo<DP>::WAVES) void is_k15_held_atten
   }
 }
 
-template <typename F>
-hipError_t for_padded(int dp, F &&f) {
-  switch (dp) {
-    case 32: return f(std::integral_constant<int, 32>{});
-    case 64: return f(std::integral_constant<int, 64>{});
-    case 96: return f(std::integral_constant<int, 96>{});
-    case 128: return f(std::integral_constant<int, 128>{});
-    case 160: return f(std::integral_constant<int, 160>{});
-    case 192: return f(std::integral_constant<int, 192>{});
-    case 224: return f(std::integral_constant<int, 224>{});
-    default: return f(std::integral_constant<int, 256>{});
-  }
-}
-
 template <typename T>
 hipError_t launch_t(const HeldPlan &p, const Args &a, hipStream_t s) {
   const dim3 grid((unsigned)(p.workgroups * p.splits));
