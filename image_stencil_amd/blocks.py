@@ -47,8 +47,9 @@ def dense_workspace_size(plan):
 
 
 def dense_get_plan_info(plan):
-    """grid: (workgroups over all tiles and entries, parts of the inner sum, 1);
-    tile: (features, rows)."""
+    """grid: (tiles of all entries, parts of the inner sum, 1); tile: (features, rows).
+    is_k13_dense_few has a workgroup for every tile; those of is_k13_dense, as many as
+    the device holds at a time, walk the tiles of all parts."""
     info = conv2d_plan_info()
     _abi.check(_abi.load().dense_get_plan_info(plan, ctypes.byref(info)), "dense_get_plan_info")
     return {"kernel": info.kernel.decode(), "grid": (info.grid_x, info.grid_y, info.grid_z), "block": info.block,
@@ -102,6 +103,10 @@ class BlockNorm:
 
         x_out = x + residual_scale * gate * post(y)
         out   = norm(x_out) * weight * (1 + scale) + shift + bias
+
+    (The bias is not scaled. A norm with weight and bias that is modulated afterwards,
+    (norm(x_out) * weight + bias) * (1 + scale) + shift, is had without bias and with
+    shift + bias * (1 + scale), rounded to its type, as the shift.)
 
     norm: "rms", "layer" or None (the sum alone); post: "rms", "layer" (the norm of
     the block's output y, times post_weight) or None. Serves rows of any number and

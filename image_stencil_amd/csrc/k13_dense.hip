@@ -12,20 +12,23 @@
 // one and a half steps ahead, also from one tile to the next. The last quarter of a step
 // runs after the barrier that frees its slots: its products cover the first operand reads
 // of the next step. Results pass the one free slot as fp32, a wave's own part, so that
-// residual and output are touched by 4 lanes a token; nothing waits for their stores.
+// residual and output are touched by 4 lanes a token. Their stores have the first step of
+// the next tile to complete in: the wait at its end leaves only that step's own loads open.
 //
 // Few rows (is_k13_dense_few): the weights are read once, straight into registers,
 // 16 features x 32 inputs an instruction (v_mfma_f32_16x16x32); the waves of a
 // workgroup take the inner sum in turn and join in LDS.
 //
-// What bounds it, measured on MI355Xs (bf16, inputs changing from call to call): 65536
-// rows, 4096 to 1024, with residual: 448 to 468 us, 1.17 to 1.23 PFLOP/s; 8192 cubed 809
-// to 841, 1.31 to 1.36 PFLOP/s: matrix cores 77% busy at 1.4 to 1.7 GHz, which the power
-// limit sets (a library product without residual: 377 and 690). Two 3600-token frames, 512
-// to 2048: 22.9 us without an activation, 23.2 ReLU, 26.2 SiLU, 26.7 tanh-GELU, 29.0 GELU (an
-// end that knows of no residual and shorter activations: 23.5, 24.1, 26.4, 27.3, 30.5 before);
-// 8 steps are 12.4 of it, the write of a whole tile per CU much of the rest. 16 rows, 8192 to 8192: 33, 4.1 TB/s (one row 28): the
-// 16 rows of x, read again by each workgroup, are as many requests as half the weights.
+// What bounds it, measured on several MI355Xs (bf16, inputs changing from call to call):
+// 65536 rows, 4096 to 1024, with residual: 448 to 468 us, 1.17 to 1.23 PFLOP/s, matrix cores
+// 67% busy; 8192 cubed 804 to 841, 1.31 to 1.37 PFLOP/s, 77% busy at 1.4 to 1.7 GHz, which
+// the power limit sets (a library product without residual: 376 and 688). Two 3600-token
+// frames, 512 to 2048: 21.6 to 22.9 us without an activation, ReLU 0.3 more, SiLU 3.3,
+// tanh-GELU 3.8, GELU 5.6 to 6.1 (an end that knows of no residual and shorter activations:
+// 23.5, 24.1, 26.4, 27.3, 30.5 before, 22.9, 23.2, 26.2, 26.7, 29.0 after); 8 steps are 12.4 of
+// it, the write of a whole tile per CU much of the rest. 16 rows, 8192 to 8192: 33, 4.1 TB/s
+// (one row 28 to 30; a library product of 16 rows 29 to 30): the 16 rows of x, read again by
+// each workgroup, are as many requests as half the weights.
 // Steps that were taken back: touching the lines of later steps (a dword of each, 892 to
 // 1050); both quarters of an accumulator's half step one after the other (841 to 874); weights
 // of few rows past the caches (33.6 to 35.9: an instruction takes half of each line).
@@ -629,7 +632,10 @@ hipError_t launch_t(const DensePlan &p, const Args &a, hipStream_t s) {
 }  // namespace
 
 // How a call is cut, by an estimate of its time in microseconds fitted to runs of 16 to
-// 65536 rows, 344 to 8192 inputs and 300 to 8192 features (most within 15%):
+// 65536 rows, 344 to 8192 inputs and 300 to 8192 features. Of 60 calls drawn from that range
+// 41 come within 15% of it and all within 31%; short calls and those of one round of large
+// tiles end sooner (33 said, 23 measured for 7200 rows, 512 to 2048), 128-squared tiles with
+// more than 4000 inputs later.
 //   tiles of 256, 128 and 64 squared, a step of 64 inputs: 1.0, 0.47 and 0.36 with one
 //     workgroup on its CU and few CUs busy, 1.55, 0.95 and 0.80 with all of them (the clock
 //     falls; two and four workgroups a CU for the smaller tiles); 4, 1.5 and 1 to fill the
@@ -638,8 +644,9 @@ hipError_t launch_t(const DensePlan &p, const Args &a, hipStream_t s) {
 //     hidden by two fifths;
 //   few rows: a workgroup takes in 40 GB/s, two on a CU 30 each;
 //   3 for a launch, 4 and the parts at 4 TB/s for joining.
-// E.g. 7200 rows, 512 to 2048: 256 squared 28 us, 128 squared 32, 64 squared 46; 300 rows,
-// 4096 to 1024: 64 squared in four parts 19 us, 128 squared in four 20, unsplit 33 and 39.
+// Measured on both sides: 7200 rows, 512 to 2048: 256 squared 21.6 us, 128 squared 24.4, 64
+// squared 31.5; 300 rows, 4096 to 1024: 64 squared in four parts 17.5 us, 128 squared in four
+// 19.4, unsplit 32.1 and 37.8.
 double least_us(const dense_desc &d) {
   return 2.0 * ((double)d.in * d.features + (double)d.n * d.len * (d.in + d.features)) / 5.0e6;
 }

@@ -495,7 +495,9 @@ typedef struct {
  *     out   = norm(x_out) * weight * (1 + scale[b]) + shift[b] + bias
  * where post and norm are 0 (for post: y as it is; for norm: no out), IS_NORM_RMS
  * or IS_NORM_LAYER over the c channels, post(y) times post_weight. The norm sees
- * x_out before it is rounded.
+ * x_out before it is rounded. The bias is not scaled: an affine norm that is modulated
+ * afterwards, (norm(x_out) * weight + bias) * (1 + scale[b]) + shift[b], is had without
+ * bias and with shift[b] + bias * (1 + scale[b]), rounded to its type, as the shift.
  *  dtype       : IS_F32, IS_F16 or IS_BF16 of x, y, x_out, out, gate, scale, shift
  *  y           : NULL: no block before; x_out = x is not written (x_out NULL)
  *  x_out       : NULL with y given: the sum is normed and not kept
@@ -562,9 +564,14 @@ typedef struct dense_plan_s *dense_plan;
 is_status dense_create(const dense_desc *d, dense_plan *out);
 void dense_destroy(dense_plan plan);
 
-/* Device bytes of workspace: 0 unless few rows and features meet long sums, which
- * are then split over workgroups and joined. */
+/* Device bytes of workspace: 0 unless rows and features make too few tiles for the
+ * device, and the sums are split over workgroups and joined: then 4 bytes a result
+ * and part (256 rows, 4096 to 4096, in four parts: 16 MB). */
 is_status dense_workspace_size(dense_plan plan, size_t *bytes);
+
+/* What the plan launches. grid_x counts the tiles of all entries and grid_y the parts
+ * of the sums: is_k13_dense_few has a workgroup for each tile, those of is_k13_dense,
+ * as many as the device holds at a time, walk them all. */
 is_status dense_get_plan_info(dense_plan plan, conv2d_plan_info *info);
 
 /* Enqueue on `stream`. x and w may be NULL when they have no element; the
@@ -615,7 +622,11 @@ is_status held_load(const held_states_desc *d, const void *held, size_t held_byt
  * tensors that held_load gives, over all `len` tokens of the store or those that
  * key_lengths and key_mask leave; masked tokens may never have been stored.
  *  lq, hq     : queries of an entry and query heads, hq % held.heads == 0
- *  scale, strides of q and out, masks, lse and workspace: as for cross_attention_* */
+ *  scale, strides of q and out, masks, lse and workspace: as for cross_attention_*
+ * As there, probabilities are rounded to the data type for the second product. With
+ * few rows the held bytes are read directly, up to each entry's length; with many
+ * (get_plan_info names what is launched) all `len` tokens are first loaded into the
+ * workspace, twice the held bytes, at every call and whatever the lengths. */
 typedef struct {
   held_states_desc held;
   int lq, hq;
